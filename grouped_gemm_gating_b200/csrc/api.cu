@@ -14,6 +14,14 @@
 #include "common.cuh"
 #include "fused.h"
 #include "gemm.h"
+#include "host.h"
+
+using moe::aligned16;
+using moe::finish;
+using moe::kWsAlign;
+using moe::num_sms_current_device;
+using moe::round_up;
+using moe::StageScope;
 
 namespace {
 
@@ -51,39 +59,6 @@ bool take_event(cudaEvent_t* ev) {
   return cudaEventCreate(ev) == cudaSuccess;
 }
 
-struct StageScope {
-  StageRecord rec{};
-  cudaStream_t stream;
-  bool active;
-  StageScope(int stage, cudaStream_t s) : stream(s), active(g_profile) {
-    if (!active) return;
-    rec.stage = stage;
-    if (!take_event(&rec.start)) {
-      active = false;
-      return;
-    }
-    if (!take_event(&rec.stop)) {
-      g_event_pool.push_back(rec.start);
-      active = false;
-      return;
-    }
-    if (record_event(rec.start, stream) != cudaSuccess) {
-      g_event_pool.push_back(rec.start);
-      g_event_pool.push_back(rec.stop);
-      active = false;
-    }
-  }
-  ~StageScope() {
-    if (!active) return;
-    if (record_event(rec.stop, stream) == cudaSuccess) {
-      g_records.push_back(rec);
-    } else {
-      g_event_pool.push_back(rec.start);
-      g_event_pool.push_back(rec.stop);
-    }
-  }
-};
-
 void release_records() {
   for (auto& r : g_records) {
     g_event_pool.push_back(r.start);
@@ -107,18 +82,6 @@ EncodeTiledFn encode_fn() {
       fn = reinterpret_cast<EncodeTiledFn>(p);
   });
   return fn;
-}
-
-int num_sms_current_device() {
-  static std::atomic<int> cache[64];  // per device; concurrent first calls store the same value
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-  int n = cache[dev].load(std::memory_order_relaxed);
-  if (n == 0) {
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    cache[dev].store(n, std::memory_order_relaxed);
-  }
-  return n;
 }
 
 // bf16 tensor [depth, rows, K] (K innermost) as a 3-D map with 64 x box_rows
@@ -162,8 +125,6 @@ bool encode_3d_u8(CUtensorMap* map, const void* base, uint64_t inner, uint64_t r
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 // fp8 expert weights (e4m3 values [E, rows, K] and their scale bytes
 // [E, K / 32, rows]) for the fused expert kernel.
 struct Fp8Weights {
@@ -173,14 +134,11 @@ struct Fp8Weights {
 
 bool valid_block_m(int bm) { return bm == 16 || bm == 32 || bm == 64 || bm == 128; }
 
-constexpr size_t kWsAlign = 256;
 // The forward workspace starts with a fixed block of int32 counters that the
 // fused expert kernel keeps at zero between calls (the last CTA of every
 // launch resets them; it uses the first three as grid counters, the rest is
 // reserved).  h (block_m = 128) and the fp32 accumulator follow it.
 constexpr size_t kCounterInts = 16384;
-
-size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 // The token-major GEMMs run on CTA pairs when the layer is wide enough for
 // the K loops to dominate a tile: d_ff >= 1024 for both GEMMs (and d >= 1024
@@ -206,12 +164,6 @@ moe_status check_dims(int T, int d, int F, int E, int k) {
   if (E > MOE_MAX_EXPERTS || k > MOE_MAX_TOPK) return MOE_ERR_UNSUPPORTED;
   if (d % 64 || F % 64 || d > 16384 || F > 16384) return MOE_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(T) * k >= (int64_t(1) << 30)) return MOE_ERR_UNSUPPORTED;
-  return MOE_OK;
-}
-
-moe_status finish(cudaError_t err, int launches) {
-  if (err != cudaSuccess) return MOE_ERR_CUDA;
-  g_last_launches = launches;
   return MOE_OK;
 }
 
@@ -268,7 +220,71 @@ BwdLayout bwd_layout(int T, int d, int F, int E, int k, moe_act act, int n_share
 }  // namespace
 
 namespace moe {
+StageScope::StageScope(int stage_id, cudaStream_t s) : stage(stage_id), stream(s), active(g_profile) {
+  if (!active) return;
+  if (!take_event(&start)) {
+    active = false;
+    return;
+  }
+  if (!take_event(&stop)) {
+    g_event_pool.push_back(start);
+    active = false;
+    return;
+  }
+  if (record_event(start, stream) != cudaSuccess) {
+    g_event_pool.push_back(start);
+    g_event_pool.push_back(stop);
+    active = false;
+  }
+}
+
+StageScope::~StageScope() {
+  if (!active) return;
+  if (record_event(stop, stream) == cudaSuccess) {
+    g_records.push_back({stage, start, stop});
+  } else {
+    g_event_pool.push_back(start);
+    g_event_pool.push_back(stop);
+  }
+}
+
 void record_launches(int n) { g_last_launches = n; }
+
+moe_status finish(cudaError_t err, int launches) {
+  if (err != cudaSuccess) return MOE_ERR_CUDA;
+  g_last_launches = launches;
+  return MOE_OK;
+}
+
+int num_sms_current_device() {
+  static std::atomic<int> cache[64];  // per device; concurrent first calls store the same value
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  int n = cache[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    cache[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+bool encode_16bit(CUtensorMap* map, bool fp16, const void* base, int rank, const uint64_t* dims,
+                  const uint64_t* strides, const uint32_t* box) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t d[4], st[4];
+  cuuint32_t bx[4], estr[4];
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    bx[i] = box[i];
+    estr[i] = 1;
+    if (i + 1 < rank) st[i] = strides[i];
+  }
+  return fn(map, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+            static_cast<cuuint32_t>(rank), const_cast<void*>(base), d, st, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 // Set by moe_debug_timeouts; read when a launch's arguments are filled.
 std::atomic<uint64_t> g_wait_limit_ns{kWaitLimitNs};

@@ -1,0 +1,9 @@
+#include "dense_gemm.cuh"
+
+namespace moe {
+
+cudaError_t launch_dense_dw(const DenseProblem& p, int num_sms, cudaStream_t stream) {
+  return dense::launch_kind<kDenseLinear, kMajorMN>(p, num_sms, stream);
+}
+
+}  // namespace moe

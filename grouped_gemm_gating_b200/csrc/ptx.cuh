@@ -360,5 +360,10 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool a_mn = 
          (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// The same for fp16 (format 0) or bf16 (format 1) A and B.
+__host__ __device__ constexpr uint32_t idesc_16bit_f32(int M, int N, bool fp16, bool a_mn, bool b_mn) {
+  return fp16 ? idesc_bf16_f32(M, N, a_mn, b_mn) & ~((1u << 7) | (1u << 10)) : idesc_bf16_f32(M, N, a_mn, b_mn);
+}
+
 }  // namespace ptx
 }  // namespace moe

@@ -23,6 +23,12 @@ ACT_SWIGLU = 0
 ACT_RELU2 = 1
 GROUP_MAX = 0
 GROUP_TOP2SUM = 1
+# activations of the dense operators
+EPI_NONE, EPI_SILU, EPI_GELU, EPI_GELU_TANH, EPI_RELU, EPI_RELU2 = range(6)
+NORM_L2 = 0
+NORM_MAX = 1
+
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 _STATUS = {
     0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED", 3: "MOE_ERR_WORKSPACE",
@@ -32,6 +38,7 @@ _STATUS = {
 # name -> (restype, argtypes)
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_int64
 _SIG = {
     "moe_max_padded": (ctypes.c_int64, [_I, _I, _I, _I]),
     "moe_align_workspace_size": (ctypes.c_size_t, [_I, _I, _I]),
@@ -53,6 +60,19 @@ _SIG = {
                              _I, _P, _P, ctypes.c_size_t, _P, _P]),
     "moe_layer_fp8": (_I, [_P, _I, _I, _I, _I, _I, _I, _I, ctypes.c_float, _P, _I, _P, _P, _P, _P, _I, _P, _P, _P,
                            _P, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P, _P]),
+    "moe_linear": (_I, [_P, _L, _L, _I, _P, _I, _P, _P, _L, _I, _I, _P, _P, _L, _P, _P]),
+    "moe_linear_backward_workspace_size": (ctypes.c_size_t, [_L, _I, _I, _I, _I]),
+    "moe_linear_backward": (_I, [_P, _L, _L, _I, _P, _I, _I, _I, _P, _P, _L, _P, _L, _P, _L, _P, _P, _P,
+                                 ctypes.c_size_t, _P, _P]),
+    "moe_ffn": (_I, [_P, _L, _L, _I, _P, _P, _I, _I, _I, _P, _L, _P, _P, _P, _L, _P, _P]),
+    "moe_ffn_backward_workspace_size": (ctypes.c_size_t, [_L, _I, _I]),
+    "moe_ffn_backward": (_I, [_P, _L, _L, _I, _P, _P, _I, _I, _I, _P, _P, _L, _P, _L, _P, _L, _P, _P, _P,
+                              ctypes.c_size_t, _P, _P]),
+    "moe_grad_plan_size": (ctypes.c_size_t, [_I]),
+    "moe_grad_plan": (_I, [_P, _P, _P, _P, _I, _P, ctypes.c_size_t, _P, _P]),
+    "moe_grad_workspace_size": (ctypes.c_size_t, []),
+    "moe_grad_norm": (_I, [_P, _I, _L, _I, _P, _P, ctypes.c_size_t, _P, _P]),
+    "moe_grad_clip": (_I, [_P, _I, _L, _I, ctypes.c_float, _P, _P, ctypes.c_size_t, _P, _P]),
     "moe_read_status": (_I, [_P, _P]),
     "moe_status_string": (ctypes.c_char_p, [_I]),
     "moe_last_launch_count": (_I, []),
@@ -62,7 +82,8 @@ _SIG = {
 }
 
 STAGES = ("route", "align", "gate_up_gemm", "down_gemm", "combine", "route_align", "fused_expert", "permute",
-          "router", "bwd_recompute", "bwd_dh_gemm", "bwd_dx_gemm", "bwd_dw13_gemm", "bwd_dw2_gemm")
+          "router", "bwd_recompute", "bwd_dh_gemm", "bwd_dx_gemm", "bwd_dw13_gemm", "bwd_dw2_gemm",
+          "linear", "ffn_gate", "dense_backward", "grad_clip")
 
 _lib = None
 _lock = threading.Lock()
@@ -329,6 +350,10 @@ class MoEGradBuffers:
             raise ValueError("unsupported layer shape")
         self.ws = torch.empty(n, dtype=torch.uint8, device=dev)
 
+    def grads(self):
+        """The weight gradients, e.g. for GradClip."""
+        return [t for t in (self.dw13, self.dw2, self.dw13_shared, self.dw2_shared) if t is not None]
+
     def backward(self, fwd: "MoEBuffers", x, w13, w2, dout, w13_shared=None, w2_shared=None):
         """Gradients of the layer whose routing and align outputs fwd holds
         (block_m = 128)."""
@@ -378,6 +403,268 @@ def moe_layer_fp8(logits, x, wq: Fp8Experts, k, block_m, act, topk_ids, topk_wei
         _ptr(topk_weights), _ptr(sorted_token_ids), _ptr(expert_ids), _ptr(num_tokens_post_padded), _ptr(inv_pos),
         _ptr(_bits(out)), _ptr(ws), ws.numel() * ws.element_size(), _ptr(dev_status), _stream(x.device))
     _check("moe_layer_fp8", code)
+
+
+# ------------------------------------------------- dense operators -------
+
+def _rows(fn, name, t, T, cols, like):
+    """(pointer, row stride) of a [T, cols] matrix of like's type and device
+    whose rows are contiguous; None -> (None, 0)."""
+    if t is None:
+        return None, 0
+    if t.dim() != 2 or t.shape[0] != T or t.shape[1] != cols:
+        raise ValueError(f"{fn}: {name} must be [{T}, {cols}], got {list(t.shape)}")
+    if t.dtype != like.dtype or t.device != like.device:
+        raise ValueError(f"{fn}: {name} must be {like.dtype} on {like.device}")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{fn}: {name}'s rows must be contiguous")
+    return t.data_ptr(), t.stride(0) if T > 1 else max(cols, 8)
+
+
+def _whole(fn, name, t, shape, like):
+    """Pointer of a contiguous tensor of the given shape, like's type and
+    device; None -> None."""
+    if t is None:
+        return None
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} must be a contiguous {list(shape)} tensor, got {list(t.shape)}")
+    if t.dtype != like.dtype or t.device != like.device:
+        raise ValueError(f"{fn}: {name} must be {like.dtype} on {like.device}")
+    return t.data_ptr()
+
+
+def _dense_args(fn, x, w, dev_status):
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError(f"{fn}: expected 2-D tensors")
+    if not x.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    if x.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"{fn}: expected bfloat16 or float16 tensors")
+    return _DTYPES[x.dtype], _status(fn, dev_status, x.device)
+
+
+def _status(fn, dev_status, device):
+    if dev_status is None:
+        return None
+    if dev_status.dtype != torch.int32 or dev_status.numel() < 1 or dev_status.device != device:
+        raise ValueError(f"{fn}: dev_status must be an int32 tensor on {device}")
+    return dev_status.data_ptr()
+
+
+def _ws(fn, ws, device):
+    if ws is None:
+        return None, 0
+    if ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"{fn}: ws must be a contiguous tensor on {device}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def moe_linear(x, w, out, bias=None, residual=None, act=EPI_NONE, pre=None, dev_status=None):
+    """out [T, N] = act(x [T, K] . w [N, K]^T + bias) + residual (out may be
+    the residual); pre [T, N], when given, keeps x . w^T + bias."""
+    fn = "moe_linear"
+    dt, status = _dense_args(fn, x, w, dev_status)
+    (T, K), N = x.shape, w.shape[0]
+    px, ldx = _rows(fn, "x", x, T, K, x)
+    pr, ldr = _rows(fn, "residual", residual, T, N, x)
+    po, ldo = _rows(fn, "out", out, T, N, x)
+    with torch.cuda.device(x.device):
+        code = load_library().moe_linear(
+            px, ldx, T, K, _whole(fn, "w", w, (N, K), x), N, _whole(fn, "bias", bias, (N,), x), pr, ldr, act, dt,
+            _whole(fn, "pre", pre, (T, N), x), po, ldo, status, _stream(x.device))
+    _check(fn, code)
+
+
+def moe_linear_backward_workspace_size(T, K, N, act, has_bias) -> int:
+    return int(load_library().moe_linear_backward_workspace_size(T, K, N, act, 1 if has_bias else 0))
+
+
+def moe_linear_backward(x, w, dout, dx=None, dw=None, dbias=None, act=EPI_NONE, pre=None, ws=None, dx_residual=None,
+                        dev_status=None):
+    """Gradients of moe_linear: dx = dz . w (+ dx_residual), dw = dz^T . x,
+    dbias = column sums of dz, with dz = dout * act'(pre); those left None
+    are not computed."""
+    fn = "moe_linear_backward"
+    dt, status = _dense_args(fn, x, w, dev_status)
+    (T, K), N = x.shape, w.shape[0]
+    px, ldx = _rows(fn, "x", x, T, K, x)
+    pd, ldd = _rows(fn, "dout", dout, T, N, x)
+    pr, lddr = _rows(fn, "dx_residual", dx_residual, T, K, x)
+    pdx, lddx = _rows(fn, "dx", dx, T, K, x)
+    pws, nws = _ws(fn, ws, x.device)
+    with torch.cuda.device(x.device):
+        code = load_library().moe_linear_backward(
+            px, ldx, T, K, _whole(fn, "w", w, (N, K), x), N, act, dt, _whole(fn, "pre", pre, (T, N), x), pd, ldd,
+            pr, lddr, pdx, lddx, _whole(fn, "dw", dw, (N, K), x), _whole(fn, "dbias", dbias, (N,), x), pws, nws,
+            status, _stream(x.device))
+    _check(fn, code)
+
+
+class LinearBuffers:
+    """Device buffers of one linear layer's shape, allocated once (plumbing
+    only): the output and, for training, the pre-activation, the gradients
+    and the backward's workspace."""
+
+    def __init__(self, T, K, N, act=EPI_NONE, dtype=torch.bfloat16, train=False, bias=False, device="cuda"):
+        self.T, self.K, self.N, self.act = T, K, N, act
+        dev = torch.device(device)
+        kw = dict(dtype=dtype, device=dev)
+        self.out = torch.empty((T, N), **kw)
+        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.pre = self.dx = self.dw = self.dbias = self.ws = None
+        if train:
+            self.pre = torch.empty((T, N), **kw) if act != EPI_NONE else None
+            self.dx = torch.empty((T, K), **kw)
+            self.dw = torch.empty((N, K), **kw)
+            self.dbias = torch.empty(N, **kw) if bias else None
+            n = moe_linear_backward_workspace_size(T, K, N, act, bias)
+            self.ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+
+    def forward(self, x, w, bias=None, residual=None):
+        moe_linear(x, w, self.out, bias, residual, self.act, self.pre, self.status)
+        return self.out
+
+    def backward(self, x, w, dout, pre=None, dx_residual=None):
+        """Fills dx, dw (and dbias); pre defaults to the last forward's."""
+        moe_linear_backward(x, w, dout, self.dx, self.dw, self.dbias, self.act, self.pre if pre is None else pre,
+                            self.ws, dx_residual, self.status)
+        return self.dx, self.dw, self.dbias
+
+
+def moe_ffn(x, w13, w2, h, out, act=EPI_SILU, residual=None, pre=None, dev_status=None):
+    """The dense gated block: h [T, F] = act(x . Wg^T) * (x . Wu^T), out [T, d]
+    = h . w2^T + residual, w13 [2F, d] holding Wg's rows, then Wu's; pre
+    [T, 2F], when given, keeps both projections for moe_ffn_backward."""
+    fn = "moe_ffn"
+    dt, status = _dense_args(fn, x, w2, dev_status)
+    (T, d), F = x.shape, w2.shape[1]
+    px, ldx = _rows(fn, "x", x, T, d, x)
+    pr, ldr = _rows(fn, "residual", residual, T, d, x)
+    po, ldo = _rows(fn, "out", out, T, d, x)
+    with torch.cuda.device(x.device):
+        code = load_library().moe_ffn(
+            px, ldx, T, d, _whole(fn, "w13", w13, (2 * F, d), x), _whole(fn, "w2", w2, (d, F), x), F, act, dt, pr, ldr,
+            _whole(fn, "pre", pre, (T, 2 * F), x), _whole(fn, "h", h, (T, F), x), po, ldo, status, _stream(x.device))
+    _check(fn, code)
+
+
+def moe_ffn_backward_workspace_size(T, d, F) -> int:
+    return int(load_library().moe_ffn_backward_workspace_size(T, d, F))
+
+
+def moe_ffn_backward(x, w13, w2, pre, dout, ws, dx=None, dw13=None, dw2=None, act=EPI_SILU, dx_residual=None,
+                     dev_status=None):
+    """Gradients of moe_ffn from the kept pre = [g | u]; those left None are
+    not computed."""
+    fn = "moe_ffn_backward"
+    dt, status = _dense_args(fn, x, w2, dev_status)
+    (T, d), F = x.shape, w2.shape[1]
+    px, ldx = _rows(fn, "x", x, T, d, x)
+    pd, ldd = _rows(fn, "dout", dout, T, d, x)
+    pr, lddr = _rows(fn, "dx_residual", dx_residual, T, d, x)
+    pdx, lddx = _rows(fn, "dx", dx, T, d, x)
+    pws, nws = _ws(fn, ws, x.device)
+    with torch.cuda.device(x.device):
+        code = load_library().moe_ffn_backward(
+            px, ldx, T, d, _whole(fn, "w13", w13, (2 * F, d), x), _whole(fn, "w2", w2, (d, F), x), F, act, dt,
+            _whole(fn, "pre", pre, (T, 2 * F), x), pd, ldd, pr, lddr, pdx, lddx,
+            _whole(fn, "dw13", dw13, (2 * F, d), x), _whole(fn, "dw2", dw2, (d, F), x), pws, nws, status,
+            _stream(x.device))
+    _check(fn, code)
+
+
+class FFNBuffers:
+    """Device buffers of one dense gated block's shape, allocated once
+    (plumbing only): h, the output and, for training, the kept projections,
+    the gradients and the backward's workspace."""
+
+    def __init__(self, T, d, F, act=EPI_SILU, dtype=torch.bfloat16, train=False, device="cuda"):
+        self.T, self.d, self.F, self.act = T, d, F, act
+        dev = torch.device(device)
+        kw = dict(dtype=dtype, device=dev)
+        self.h = torch.empty((T, F), **kw)
+        self.out = torch.empty((T, d), **kw)
+        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.pre = self.dx = self.dw13 = self.dw2 = self.ws = None
+        if train:
+            self.pre = torch.empty((T, 2 * F), **kw)
+            self.dx = torch.empty((T, d), **kw)
+            self.dw13 = torch.empty((2 * F, d), **kw)
+            self.dw2 = torch.empty((d, F), **kw)
+            n = moe_ffn_backward_workspace_size(T, d, F)
+            if n == 0:
+                raise ValueError("unsupported block shape")
+            self.ws = torch.empty(n, dtype=torch.uint8, device=dev)
+
+    def forward(self, x, w13, w2, residual=None):
+        moe_ffn(x, w13, w2, self.h, self.out, self.act, residual, self.pre, self.status)
+        return self.out
+
+    def backward(self, x, w13, w2, dout, pre=None, dx_residual=None):
+        """Fills dx, dw13 and dw2; pre defaults to the last forward's."""
+        moe_ffn_backward(x, w13, w2, self.pre if pre is None else pre, dout, self.ws, self.dx, self.dw13, self.dw2,
+                         self.act, dx_residual, self.status)
+        return self.dx, self.dw13, self.dw2
+
+
+class GradClip:
+    """Global norm and clipping of a set of gradient tensors: the plan (which
+    holds the tensors' addresses, and the tensors with them), its workspace
+    and the norm.  outs: where the scaled tensors go (default: in place).
+    Make a new one when a gradient buffer is replaced."""
+
+    def __init__(self, grads, outs=None):
+        grads = list(grads)
+        outs = grads if outs is None else list(outs)
+        if not grads or len(outs) != len(grads):
+            raise ValueError("GradClip: one or more gradients, and as many targets")
+        dev = grads[0].device
+        if dev.type != "cuda":
+            raise ValueError("expected a CUDA tensor")
+        for g, o in zip(grads, outs):
+            if g.dtype not in _DTYPES:
+                raise ValueError("GradClip: bfloat16, float16 or float32 tensors")
+            if o.dtype != g.dtype or o.shape != g.shape or g.device != dev or o.device != dev:
+                raise ValueError("GradClip: a target has its gradient's shape, type and device")
+            if not g.is_contiguous() or not o.is_contiguous():
+                raise ValueError("expected a contiguous tensor")
+        n = len(grads)
+        self.n, self.device, self._held = n, dev, (grads, outs)
+        lib = load_library()
+        src = (ctypes.c_void_p * n)(*[g.data_ptr() for g in grads])
+        dst = (ctypes.c_void_p * n)(*[o.data_ptr() for o in outs])
+        numel = (ctypes.c_int64 * n)(*[g.numel() for g in grads])
+        dtype = (ctypes.c_int32 * n)(*[_DTYPES[g.dtype] for g in grads])
+        size = int(lib.moe_grad_plan_size(n))
+        self.plan = torch.empty(max(size, 1), dtype=torch.uint8, device=dev)
+        self.ws = torch.empty(int(lib.moe_grad_workspace_size()), dtype=torch.uint8, device=dev)
+        self.total_norm = torch.zeros((), dtype=torch.float32, device=dev)
+        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        chunks = ctypes.c_int64(0)
+        with torch.cuda.device(dev):
+            code = lib.moe_grad_plan(src, dst, numel, dtype, n, self.plan.data_ptr(), size, ctypes.byref(chunks),
+                                     _stream(dev))
+        _check("moe_grad_plan", code)
+        self.chunks = chunks.value
+
+    def norm(self, norm_type=NORM_L2):
+        """The global norm (a 0-d fp32 tensor on the device)."""
+        with torch.cuda.device(self.device):
+            code = load_library().moe_grad_norm(
+                self.plan.data_ptr(), self.n, self.chunks, norm_type, self.total_norm.data_ptr(), self.ws.data_ptr(),
+                self.ws.numel(), self.status.data_ptr(), _stream(self.device))
+        _check("moe_grad_norm", code)
+        return self.total_norm
+
+    def clip(self, max_norm, norm_type=NORM_L2):
+        """Scales the gradients to a global norm of at most max_norm; returns
+        the norm before (a 0-d fp32 tensor on the device)."""
+        with torch.cuda.device(self.device):
+            code = load_library().moe_grad_clip(
+                self.plan.data_ptr(), self.n, self.chunks, norm_type, float(max_norm), self.total_norm.data_ptr(),
+                self.ws.data_ptr(), self.ws.numel(), self.status.data_ptr(), _stream(self.device))
+        _check("moe_grad_clip", code)
+        return self.total_norm
 
 
 def moe_read_status(dev_status) -> int:

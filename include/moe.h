@@ -75,7 +75,7 @@ typedef enum {
   MOE_ERR_UNSUPPORTED = 2,    /* valid arguments outside the library's limits */
   MOE_ERR_WORKSPACE = 3,      /* workspace pointer missing or too small */
   MOE_ERR_CUDA = 4,           /* a CUDA runtime/driver call failed (launch, attribute, tensor map) */
-  MOE_ERR_NONFINITE = 5,      /* device: a router logit was NaN or infinite */
+  MOE_ERR_NONFINITE = 5,      /* device: a router logit, or a gradient norm, was NaN or infinite */
   MOE_ERR_DEVICE_TIMEOUT = 6, /* device: a pipeline wait exceeded its time limit; outputs are invalid */
   MOE_ERR_BAD_EXPERT_ID = 7   /* device: a topk_ids entry was outside [0, E) */
 } moe_status;
@@ -417,6 +417,163 @@ MOE_API moe_status moe_backward(const uint16_t* x, int T, int d,
                         uint16_t* dw13_shared, uint16_t* dw2_shared, float* dtopk_weights,
                         void* ws, size_t ws_bytes, int32_t* dev_status, moe_stream_t stream);
 
+/*
+ * ---------------------------------------------------------------- dense operators
+ *
+ * What a model built around the expert layer runs next to it: the dense
+ * projections, the dense gated feed-forward block (the layers that are not
+ * split into experts, or a shared expert on its own), their training passes,
+ * and the clipping of all gradients to a global norm.
+ *
+ * Matrices here are row-major 16-bit values (moe_dtype MOE_BF16 or MOE_FP16,
+ * passed as uint16_t patterns) with a row stride `ld*` in elements, at least
+ * the number of columns; weights, `pre`, `h` and weight gradients have no
+ * gap between rows.  Column counts and strides are multiples of 8 and
+ * pointers are 16-byte aligned; T is any number up to 2^24, columns up to
+ * 2^17 (MOE_ERR_UNSUPPORTED beyond).  An output may not share memory with an
+ * input or another output (MOE_ERR_INVALID_ARG), except where stated; column
+ * slices of one row-major buffer are fine.  Sums are fp32, rounded once to
+ * the output; the results are the same on every call.  A NaN or infinity
+ * goes where the formula sends it; nothing outside a matrix's rows and
+ * columns is read into a result or written.  T == 0: outputs of T rows are
+ * no-ops, weight and bias gradients are set to zero.
+ */
+typedef enum { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2 } moe_dtype;
+
+/* Activations of the dense operators. */
+typedef enum {
+  MOE_EPI_NONE = 0,
+  MOE_EPI_SILU = 1,      /* z / (1 + e^-z) */
+  MOE_EPI_GELU = 2,      /* z (1 + erf(z / sqrt 2)) / 2 */
+  MOE_EPI_GELU_TANH = 3, /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+  MOE_EPI_RELU = 4,
+  MOE_EPI_RELU2 = 5      /* max(z, 0)^2 */
+} moe_epi_act;
+
+/*
+ * moe_linear -- out = act(x W^T + bias) + residual in one kernel.
+ *   x         [T, K]; w [N, K]; bias [N] or NULL; residual [T, N] or NULL
+ *             (row stride ldr).
+ *   pre       [T, N] out or NULL: x W^T + bias rounded to dtype, which
+ *             moe_linear_backward reads when there is an activation.
+ *   out       [T, N] out; may be the residual itself (same pointer and stride).
+ */
+MOE_API moe_status moe_linear(const uint16_t* x, int64_t ldx, int64_t T, int K, const uint16_t* w, int N,
+                      const uint16_t* bias, const uint16_t* residual, int64_t ldr,
+                      moe_epi_act act, moe_dtype dtype,
+                      uint16_t* pre, uint16_t* out, int64_t ldo,
+                      int32_t* dev_status, moe_stream_t stream);
+
+/* Bytes of scratch of moe_linear_backward (0 when it needs none, or on
+ * invalid arguments): dz [T, N] when there is an activation, and partial
+ * sums when dbias is wanted (has_bias). */
+MOE_API size_t moe_linear_backward_workspace_size(int64_t T, int K, int N, moe_epi_act act, int has_bias);
+
+/*
+ * moe_linear_backward -- with dz = dout * act'(pre):
+ *   dx = dz W (+ dx_residual)   dw = dz^T x   dbias = sum over rows of dz
+ *   pre          moe_linear's (not read with MOE_EPI_NONE: may be NULL).
+ *   dx_residual  [T, K] or NULL: added to dx before its rounding (the
+ *                gradient of a residual branch that starts at x); may be dx
+ *                itself.  Not read when dx is NULL.
+ *   dx, dw, dbias  outputs; NULL: not computed (not all three).
+ * dz is rounded to dtype for the two products (it is an operand of the
+ * tensor cores); dbias is the sum of the unrounded values.  The slope of
+ * relu and relu^2 at 0 is 0.
+ */
+MOE_API moe_status moe_linear_backward(const uint16_t* x, int64_t ldx, int64_t T, int K, const uint16_t* w, int N,
+                               moe_epi_act act, moe_dtype dtype, const uint16_t* pre,
+                               const uint16_t* dout, int64_t ldd,
+                               const uint16_t* dx_residual, int64_t lddr,
+                               uint16_t* dx, int64_t lddx, uint16_t* dw, uint16_t* dbias,
+                               void* ws, size_t ws_bytes, int32_t* dev_status, moe_stream_t stream);
+
+/*
+ * moe_ffn -- the dense gated feed-forward block
+ *   out = (act(x Wg^T) * (x Wu^T)) W2^T + residual
+ * in two kernels: both projections, the activation and the product; then the
+ * down projection with the residual.
+ *   x         [T, d]; w13 [2 F, d], rows [0, F) the gate projection Wg and
+ *             [F, 2 F) the up projection Wu (moe_forward's layout); w2 [d, F].
+ *   act       the gate's activation (MOE_EPI_SILU: SwiGLU).
+ *   residual  [T, d] or NULL; may be x.
+ *   pre       [T, 2 F] out or NULL: [x Wg^T | x Wu^T] rounded to dtype, for
+ *             moe_ffn_backward.
+ *   h         [T, F] out: act(g) * u rounded to dtype (the down projection's
+ *             operand).
+ *   out       [T, d] out; may be the residual or x itself (same pointer and
+ *             stride).
+ */
+MOE_API moe_status moe_ffn(const uint16_t* x, int64_t ldx, int64_t T, int d,
+                   const uint16_t* w13, const uint16_t* w2, int F,
+                   moe_epi_act act, moe_dtype dtype,
+                   const uint16_t* residual, int64_t ldr,
+                   uint16_t* pre, uint16_t* h, uint16_t* out, int64_t ldo,
+                   int32_t* dev_status, moe_stream_t stream);
+
+/* Bytes of scratch of moe_ffn_backward: [dg | du] [T, 2 F] and h [T, F]
+ * (0 on invalid arguments). */
+MOE_API size_t moe_ffn_backward_workspace_size(int64_t T, int d, int F);
+
+/*
+ * moe_ffn_backward -- with pre = [g | u] of moe_ffn and dh = dout W2:
+ *   dg = dh u act'(g), du = dh act(g)
+ *   dx   = [dg | du] W13 (+ dx_residual)
+ *   dw13 = [dg | du]^T x        [2 F, d]
+ *   dw2  = dout^T (act(g) u)    [d, F]
+ * dx_residual as for moe_linear_backward.  dx, dw13 and dw2 may be NULL (not
+ * all three): not computed.  dg, du and h are rounded to dtype for the
+ * products they enter.  The residual's own gradient is dout.
+ */
+MOE_API moe_status moe_ffn_backward(const uint16_t* x, int64_t ldx, int64_t T, int d,
+                            const uint16_t* w13, const uint16_t* w2, int F,
+                            moe_epi_act act, moe_dtype dtype, const uint16_t* pre,
+                            const uint16_t* dout, int64_t ldd,
+                            const uint16_t* dx_residual, int64_t lddr,
+                            uint16_t* dx, int64_t lddx, uint16_t* dw13, uint16_t* dw2,
+                            void* ws, size_t ws_bytes, int32_t* dev_status, moe_stream_t stream);
+
+/*
+ * Gradient clipping.  A plan lists n tensors (any sizes, empty ones among
+ * them; bf16, fp16 and fp32 may be mixed; element alignment is enough) and
+ * where their scaled values go; it is made once for a set of buffers and
+ * holds their addresses, so it is made again when a buffer moves.
+ *
+ * moe_grad_plan -- writes the plan (device memory, moe_grad_plan_size bytes,
+ * 16-byte aligned) and, on the host, the number of chunks the other calls
+ * take.
+ *   src, numel, dtype  host arrays of n device pointers, element counts and
+ *                      moe_dtype values.
+ *   dst                host array of n targets, or NULL: in place.  A target
+ *                      is its source or does not overlap it, and no target
+ *                      overlaps another tensor (not checked across tensors).
+ * MOE_ERR_WORKSPACE if the plan buffer is missing or too small.
+ */
+typedef enum { MOE_NORM_L2 = 0, MOE_NORM_MAX = 1 } moe_norm_type;
+MOE_API size_t moe_grad_plan_size(int n);
+MOE_API moe_status moe_grad_plan(const void* const* src, void* const* dst, const int64_t* numel,
+                         const int32_t* dtype, int n, void* plan, size_t plan_bytes,
+                         int64_t* chunks, moe_stream_t stream);
+
+/* Bytes of scratch of moe_grad_norm and moe_grad_clip (no initial contents
+ * needed); calls sharing it must not overlap on the GPU. */
+MOE_API size_t moe_grad_workspace_size(void);
+
+/*
+ * moe_grad_norm -- norm[0] = sqrt(sum of squares), or the largest magnitude,
+ * over every element of the plan's tensors (fp32, device; sums in 64 bits,
+ * in a fixed order).
+ * moe_grad_clip -- the same norm, then every tensor scaled by
+ * c = min(1, max_norm / (norm + 1e-6)) in fp32 and rounded once into its
+ * target; with c = 1 values are copied, and tensors in place are not touched.
+ * max_norm > 0 (infinity: never scales).  If the norm is NaN or infinite,
+ * dev_status becomes MOE_ERR_NONFINITE, norm[0] holds it and c = 1.
+ */
+MOE_API moe_status moe_grad_norm(const void* plan, int n, int64_t chunks, moe_norm_type type, float* norm,
+                         void* ws, size_t ws_bytes, int32_t* dev_status, moe_stream_t stream);
+MOE_API moe_status moe_grad_clip(const void* plan, int n, int64_t chunks, moe_norm_type type, float max_norm,
+                         float* norm, void* ws, size_t ws_bytes, int32_t* dev_status, moe_stream_t stream);
+
 /* Synchronises `stream`, then returns the code stored in dev_status (MOE_OK
  * when 0), or MOE_ERR_CUDA if the synchronisation or the copy failed. */
 MOE_API moe_status moe_read_status(const int32_t* dev_status, moe_stream_t stream);
@@ -464,7 +621,10 @@ MOE_API moe_status moe_debug_timeouts(uint64_t wait_limit_ns, int unreachable_ar
  * the expert-sorted order for the gate/up GEMM on CTA pairs, and the
  * backward's row copies), 8 router (moe_router), and for moe_backward: 9
  * pre-activation recompute, 10 dh GEMM with the activation's derivative,
- * 11 dx GEMM, 12 dW13 GEMM, 13 dW2 GEMM (its conversion of dx is stage 4).
+ * 11 dx GEMM, 12 dW13 GEMM, 13 dW2 GEMM (its conversion of dx is stage 4);
+ * dense operators: 14 moe_linear (and moe_ffn's down projection), 15 moe_ffn's
+ * gate/up kernel, 16 moe_linear_backward / moe_ffn_backward (all kernels), 17
+ * moe_grad_norm / moe_grad_clip.
  * moe_profile_enable(1) starts a fresh record (and primes the event pool),
  * (0) stops recording and keeps what was recorded.  moe_profile_collect waits for the recorded events,
  * writes into stage_ms[i] (i < n_stages) the summed milliseconds of stage i
@@ -472,7 +632,7 @@ MOE_API moe_status moe_debug_timeouts(uint64_t wait_limit_ns, int unreachable_ar
  * release != 0 it then returns the events to the pool and clears the record
  * (release == 0 keeps them, e.g. to read a graph's events after each
  * replay).  MOE_ERR_CUDA if an event call failed. */
-#define MOE_NUM_STAGES 14
+#define MOE_NUM_STAGES 18
 MOE_API moe_status moe_profile_enable(int on);
 MOE_API moe_status moe_profile_collect(double* stage_ms, int* stage_calls, int n_stages, int release);
 
