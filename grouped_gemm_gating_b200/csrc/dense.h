@@ -38,6 +38,7 @@ struct DenseProblem {
   void* pre;             // linear: [M, N]; gate, gate-grad: [M, 2 N]; row stride ldp; null: not kept
   int64_t ldp;
   void* out2;            // gate-grad: h [M, N], row stride N
+  int b_ready;           // b is not written by the kernel before this one in the stream
   int32_t* status;
 };
 cudaError_t launch_dense_gemm(const DenseProblem& p, int num_sms, cudaStream_t stream, int* launches);

@@ -305,6 +305,7 @@ moe_status moe_ffn(const uint16_t* x, int64_t ldx, int64_t T, int d, const uint1
   if (err != cudaSuccess) return MOE_ERR_CUDA;
   p.epi = moe::kDenseLinear;
   p.act = MOE_EPI_NONE;
+  p.b_ready = 1;  // the gate/up kernel, which waited for all work before it, does not write w2
   p.N = d;
   p.K = F;
   p.a = h;

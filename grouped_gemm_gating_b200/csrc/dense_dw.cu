@@ -1,4 +1,4 @@
-#include "dense_gemm.cuh"
+#include "dense_split.cuh"
 
 namespace moe {
 

@@ -546,12 +546,6 @@ cudaError_t launch_variant(const DenseProblem& p, int num_sms, cudaStream_t stre
   return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
-template <int EPI, int MAJOR>
-cudaError_t launch_kind(const DenseProblem& p, int num_sms, cudaStream_t stream) {
-  return p.fp16 ? launch_variant<EPI, MAJOR, 256, true>(p, num_sms, stream)
-                : launch_variant<EPI, MAJOR, 256, false>(p, num_sms, stream);
-}
-
 }  // namespace dense
 
 // One translation unit per kind.

@@ -1,0 +1,447 @@
+// The dense GEMMs of dense_gemm.cuh for few rows or few tiles: small tiles,
+// the contraction split over the CTAs of a cluster.
+//
+// Few tokens leave a 256 x 256 tile mostly empty and most SMs without one,
+// while the weights still have to come from memory once: the call is bound
+// by their bytes (or, small enough, by latency), and every SM has to pull.
+// Here a tile is 128 output columns x BT rows, with the roles of the operands
+// swapped: the columns' operand (the weights) is the MMA's M = 128 side, the
+// rows its N = BT side (16 to 256).  A cluster of S CTAs shares one tile,
+// each contracting its part of k; the fp32 parts meet in shared memory, every
+// CTA adds the S parts of its share of the columns through distributed shared
+// memory, always in the same order, and applies the epilogue to the sum.  No
+// workspace, no atomics, the same result on every call.
+//
+// A gate tile's 128 columns are 64 rows of Wg and the matching 64 of Wu.
+#pragma once
+#include "dense_gemm.cuh"
+
+namespace moe {
+namespace dense {
+
+struct SplitArgs {
+  CUtensorMap tm_c, tm_r;  // the columns' operand, the rows' operand
+  int64_t M, N, ldr, ldo, ldp;
+  int nk;
+  const uint16_t* bias;
+  const uint16_t* residual;
+  uint16_t* out;
+  uint16_t* pre;
+  uint16_t* out2;
+  int act;
+  int early;               // columns' operand is not written by the previous kernel of the stream
+  int32_t* status;
+  uint64_t wait_ns;
+  int surplus;
+};
+
+template <int EPI, int MAJOR, int BT>
+struct SplitCfg {
+  static constexpr bool kCMn = MAJOR != kMajorKK;
+  static constexpr bool kRMn = MAJOR == kMajorMN;
+  static constexpr int kOutCols = EPI == kDenseGate ? 64 : 128;
+  static constexpr int kCBytes = 128 * 128;
+  static constexpr int kRBytes = BT * 128;
+  static constexpr int kStageBytes = kCBytes + kRBytes;
+  // two CTAs on an SM up to 64 rows, one beyond
+  static constexpr int kStages = BT <= 16 ? 6 : BT <= 32 ? 5 : BT <= 64 ? 4 : BT <= 128 ? 6 : 4;
+  static constexpr int kTmemCols = BT < 32 ? 32 : BT;
+  static constexpr int kThreads = 256;
+  static constexpr int kPartStride = 132;  // floats between two rows' sums of the 128 columns
+  static constexpr int kSmemBytes = kStages * kStageBytes + 256 + 1024;
+  static_assert(BT * kPartStride * 4 <= kStages * kStageBytes, "sums reuse the stages");
+  static_assert(!kRMn || BT % 64 == 0, "row operand chunks");
+  static_assert(kSmemBytes <= 232448, "shared memory per block");
+};
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+__device__ __forceinline__ uint32_t map_rank(uint32_t smem_addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr), "r"(rank));
+  return r;
+}
+
+template <bool kFp16>
+__device__ __forceinline__ void unpack4(uint2 v, float (&f)[4]) {
+  const float2 a = unpack2<kFp16>(v.x), b = unpack2<kFp16>(v.y);
+  f[0] = a.x;
+  f[1] = a.y;
+  f[2] = b.x;
+  f[3] = b.y;
+}
+
+template <bool kFp16>
+__device__ __forceinline__ void store4(uint16_t* p, const float (&f)[4]) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack2<kFp16>(f[0], f[1]), pack2<kFp16>(f[2], f[3]));
+}
+
+template <int EPI, int MAJOR, int BT, bool kFp16>
+__global__ void __launch_bounds__(SplitCfg<EPI, MAJOR, BT>::kThreads)
+    dense_split_kernel(const __grid_constant__ SplitArgs args) {
+  using C = SplitCfg<EPI, MAJOR, BT>;
+  constexpr uint32_t kIdesc = ptx::idesc_16bit_f32(128, BT, kFp16, C::kCMn, C::kRMn);
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kStages * C::kStageBytes);
+  uint64_t* empty = full + C::kStages;
+  uint64_t* done = empty + C::kStages;  // every MMA of this CTA
+  uint64_t* drain = done + 1;           // the same, without the test hook's surplus
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  volatile int* never = reinterpret_cast<volatile int*>(tmem_holder + 2);
+
+  const int warp = threadIdx.x / kWarp;
+  const int lane = threadIdx.x % kWarp;
+  const int S = static_cast<int>(gridDim.z);  // CTAs of a cluster: parts of k
+  const int rank = static_cast<int>(blockIdx.z);
+  const int64_t col0 = static_cast<int64_t>(blockIdx.x) * C::kOutCols;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.y) * BT;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(args.nk) * rank / S);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(args.nk) * (rank + 1) / S);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      ptx::mbar_init(&full[s], 1);
+      ptx::mbar_init(&empty[s], 1);
+    }
+    ptx::mbar_init(done, 1 + args.surplus);
+    ptx::mbar_init(drain, 1);
+    *abort_flag = 0;
+    *never = 0;
+    ptx::fence_mbar_init();
+    ptx::prefetch_tmap(&args.tm_c);
+    ptx::prefetch_tmap(&args.tm_r);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(tmem_holder, C::kTmemCols);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+  auto fail = [&]() {
+    *abort_flag = 1;
+    set_status(args.status, MOE_ERR_DEVICE_TIMEOUT);
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---------------------------------------------- TMA producer
+      auto load_c = [&](int stage, int kb) {
+        uint8_t* sC = smem + stage * C::kStageBytes;
+        if constexpr (EPI == kDenseGate) {
+          ptx::tma_load_3d(sC, &args.tm_c, &full[stage], kb * 64, static_cast<int>(col0), 0);
+          ptx::tma_load_3d(sC + 8192, &args.tm_c, &full[stage], kb * 64, static_cast<int>(col0), 1);
+        } else if constexpr (C::kCMn) {
+          ptx::tma_load_2d(sC, &args.tm_c, &full[stage], static_cast<int>(col0), kb * 64);
+          ptx::tma_load_2d(sC + 8192, &args.tm_c, &full[stage], static_cast<int>(col0) + 64, kb * 64);
+        } else {
+          ptx::tma_load_2d(sC, &args.tm_c, &full[stage], kb * 64, static_cast<int>(col0));
+        }
+      };
+      auto load_r = [&](int stage, int kb) {
+        uint8_t* sR = smem + stage * C::kStageBytes + C::kCBytes;
+        if constexpr (C::kRMn) {
+#pragma unroll
+          for (int j = 0; j < BT / 64; ++j)
+            ptx::tma_load_2d(sR + j * 8192, &args.tm_r, &full[stage], static_cast<int>(row0) + 64 * j, kb * 64);
+        } else {
+          ptx::tma_load_2d(sR, &args.tm_r, &full[stage], kb * 64, static_cast<int>(row0));
+        }
+      };
+      const int n = kb1 - kb0;
+      const int pre = n < C::kStages ? n : C::kStages;
+      // Weights that the previous kernel does not write are fetched while it
+      // still runs.
+      if (args.early)
+        for (int i = 0; i < pre; ++i) {
+          ptx::mbar_arrive_expect_tx(&full[i], C::kStageBytes);
+          load_c(i, kb0 + i);
+        }
+      pdl_wait();
+      pdl_launch_dependents();
+      for (int i = 0; i < pre; ++i) {
+        if (!args.early) {
+          ptx::mbar_arrive_expect_tx(&full[i], C::kStageBytes);
+          load_c(i, kb0 + i);
+        }
+        load_r(i, kb0 + i);
+      }
+      int issued = pre;
+      for (int i = pre; i < n; ++i) {
+        const int st = i % C::kStages;
+        if (!ptx::mbar_wait_bounded(&empty[st], ((i / C::kStages) & 1) ^ 1u, abort_flag, args.wait_ns)) {
+          fail();
+          break;
+        }
+        ptx::mbar_arrive_expect_tx(&full[st], C::kStageBytes);
+        load_c(st, kb0 + i);
+        load_r(st, kb0 + i);
+        ++issued;
+      }
+      // the last load into every stage lands before shared memory is reused
+      for (int i = issued > C::kStages ? issued - C::kStages : 0; i < issued; ++i)
+        ptx::mbar_wait_bounded(&full[i % C::kStages], (i / C::kStages) & 1, never, kDrainLimitNs);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ---------------------------------------------- MMA issuer
+      for (int i = 0; i < kb1 - kb0; ++i) {
+        const int st = i % C::kStages;
+        if (!ptx::mbar_wait_bounded(&full[st], (i / C::kStages) & 1, abort_flag, args.wait_ns)) {
+          fail();
+          break;
+        }
+        ptx::tc_fence_after();
+        const uint32_t sC = ptx::smem_u32(smem + st * C::kStageBytes);
+        const uint32_t sR = sC + C::kCBytes;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          const uint64_t dc = C::kCMn ? ptx::sw128_mnmajor_desc(sC + kk * 2048, 8192)
+                                      : ptx::sw128_kmajor_desc(sC + kk * 32);
+          const uint64_t dr = C::kRMn ? ptx::sw128_mnmajor_desc(sR + kk * 2048, 8192)
+                                      : ptx::sw128_kmajor_desc(sR + kk * 32);
+          ptx::mma_bf16(tmem_base, dc, dr, kIdesc, (i | kk) != 0 ? 1u : 0u);
+        }
+        ptx::mma_commit(&empty[st]);
+      }
+      ptx::mma_commit(done);
+      ptx::mma_commit(drain);
+      if (!ptx::mbar_wait_bounded(drain, 0u, never, kDrainLimitNs)) fail();
+    }
+  }
+  __syncwarp();
+  pdl_wait();  // the epilogue reads what earlier kernels wrote
+  if (!ptx::mbar_wait_bounded(done, 0u, abort_flag, args.wait_ns)) fail();
+  __syncthreads();  // the stages are free: every load landed, every MMA read them
+  ptx::tc_fence_after();
+
+  // ---- this CTA's sums, [row][128 columns], in place of the stages
+  float* part = reinterpret_cast<float*>(smem);
+  {
+    const int q = warp & 3;
+    constexpr int kHalf = BT >= 32 ? BT / 2 : BT;  // rows of a warp
+    if (BT >= 32 || warp < 4) {
+      const int t0 = (warp >> 2) * kHalf;
+      const uint32_t addr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(t0);
+      float* dst = part + t0 * C::kPartStride + q * 32 + lane;
+#pragma unroll 1
+      for (int c = 0; c < kHalf; c += 16) {
+        uint32_t a[16];
+        ptx::tmem_ld16(addr + c, a);
+        ptx::tmem_wait_ld();
+        pin(a);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) dst[(c + j) * C::kPartStride] = __uint_as_float(a[j]);
+      }
+    }
+  }
+  ptx::tc_fence_before();
+  ptx::cluster_sync();  // every part is there
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem_base, C::kTmemCols);
+  }
+
+  // ---- sums over the parts and the epilogue, four columns at a time; this
+  // CTA takes groups [g0, g1) of the tile's columns
+  constexpr int kGroups = C::kOutCols / 4;
+  const int g0 = kGroups * rank / S, ng = kGroups * (rank + 1) / S - g0;
+  const int64_t live = args.M - row0 < BT ? args.M - row0 : BT;
+  const uint32_t part_addr = ptx::smem_u32(part);
+  auto sum_at = [&](int t, int c, float (&v)[4]) {
+    const uint32_t off = part_addr + static_cast<uint32_t>(t * C::kPartStride + c) * 4;
+    v[0] = v[1] = v[2] = v[3] = 0.0f;
+    for (int s = 0; s < S; ++s) {
+      const float4 p = ld_cluster_f4(map_rank(off, s));
+      v[0] += p.x;
+      v[1] += p.y;
+      v[2] += p.z;
+      v[3] += p.w;
+    }
+  };
+  const int items = static_cast<int>(live) * ng;
+  if (*abort_flag == 0) {
+    with_act(EPI == kDenseLinear && MAJOR != kMajorKK ? MOE_EPI_NONE : args.act, [&](auto act) {
+      constexpr int kAct = decltype(act)::value;
+      for (int i = threadIdx.x; i < items; i += C::kThreads) {
+        const int t = i / ng;
+        const int c = (g0 + i - t * ng) * 4;
+        const int64_t row = row0 + t, col = col0 + c;
+        if (col >= args.N) continue;
+        float v[4];
+        sum_at(t, c, v);
+        if constexpr (EPI == kDenseLinear) {
+          if constexpr (MAJOR == kMajorKK) {
+            if (args.bias != nullptr) {
+              float b[4];
+              unpack4<kFp16>(*reinterpret_cast<const uint2*>(args.bias + col), b);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) v[j] += b[j];
+            }
+            if (args.pre != nullptr) store4<kFp16>(args.pre + row * args.ldp + col, v);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = act_value(v[j], kAct);
+          }
+          if (MAJOR != kMajorMN && args.residual != nullptr) {
+            float r[4];
+            unpack4<kFp16>(*reinterpret_cast<const uint2*>(args.residual + row * args.ldr + col), r);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] += r[j];
+          }
+          store4<kFp16>(args.out + row * args.ldo + col, v);
+        } else if constexpr (EPI == kDenseGate) {
+          float u[4], h[4];
+          sum_at(t, c + 64, u);
+          if (args.pre != nullptr) {
+            store4<kFp16>(args.pre + row * args.ldp + col, v);
+            store4<kFp16>(args.pre + row * args.ldp + args.N + col, u);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) h[j] = act_value(v[j], kAct) * u[j];
+          store4<kFp16>(args.out + row * args.ldo + col, h);
+        } else {
+          float g[4], u[4], dg[4], du[4], h[4];
+          unpack4<kFp16>(*reinterpret_cast<const uint2*>(args.pre + row * args.ldp + col), g);
+          unpack4<kFp16>(*reinterpret_cast<const uint2*>(args.pre + row * args.ldp + args.N + col), u);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float slope;
+            const float a = act_value_slope(g[j], kAct, &slope);
+            h[j] = a * u[j];
+            dg[j] = v[j] * u[j] * slope;
+            du[j] = v[j] * a;
+          }
+          store4<kFp16>(args.out + row * args.ldo + col, dg);
+          store4<kFp16>(args.out + row * args.ldo + args.N + col, du);
+          store4<kFp16>(args.out2 + row * args.N + col, h);
+        }
+      }
+    });
+  }
+  if (S > 1) ptx::cluster_sync();  // no CTA leaves while another reads its sums
+}
+
+template <int EPI, int MAJOR, int BT, bool kFp16>
+cudaError_t launch_split_variant(const DenseProblem& p, int S, cudaStream_t stream) {
+  using C = SplitCfg<EPI, MAJOR, BT>;
+  auto kern = dense_split_kernel<EPI, MAJOR, BT, kFp16>;
+  static std::atomic<bool> attr_done[64];
+  cudaError_t err = allow_smem(kern, C::kSmemBytes, attr_done);
+  if (err != cudaSuccess) return err;
+  SplitArgs a = {};
+  const uint64_t M = p.M, N = p.N, K = p.K;
+  bool ok;
+  if (C::kRMn) {
+    const uint64_t dims[2] = {M, K}, st[1] = {static_cast<uint64_t>(p.lda) * 2};
+    const uint32_t box[2] = {64, 64};
+    ok = encode_16bit(&a.tm_r, kFp16, p.a, 2, dims, st, box);
+  } else {
+    const uint64_t dims[2] = {K, M}, st[1] = {static_cast<uint64_t>(p.lda) * 2};
+    const uint32_t box[2] = {64, BT};
+    ok = encode_16bit(&a.tm_r, kFp16, p.a, 2, dims, st, box);
+  }
+  if (EPI == kDenseGate) {
+    const uint64_t dims[3] = {K, N, 2}, st[2] = {static_cast<uint64_t>(p.ldb) * 2, static_cast<uint64_t>(p.ldb) * 2 * N};
+    const uint32_t box[3] = {64, 64, 1};
+    ok = ok && encode_16bit(&a.tm_c, kFp16, p.b, 3, dims, st, box);
+  } else if (C::kCMn) {
+    const uint64_t dims[2] = {N, K}, st[1] = {static_cast<uint64_t>(p.ldb) * 2};
+    const uint32_t box[2] = {64, 64};
+    ok = ok && encode_16bit(&a.tm_c, kFp16, p.b, 2, dims, st, box);
+  } else {
+    const uint64_t dims[2] = {K, N}, st[1] = {static_cast<uint64_t>(p.ldb) * 2};
+    const uint32_t box[2] = {64, 128};
+    ok = ok && encode_16bit(&a.tm_c, kFp16, p.b, 2, dims, st, box);
+  }
+  if (!ok) return cudaErrorInvalidValue;
+  a.M = p.M;
+  a.N = p.N;
+  a.ldr = p.ldr;
+  a.ldo = p.ldo;
+  a.ldp = p.ldp;
+  a.nk = static_cast<int>((p.K + 63) / 64);
+  a.bias = static_cast<const uint16_t*>(p.bias);
+  a.residual = static_cast<const uint16_t*>(p.residual);
+  a.out = static_cast<uint16_t*>(p.out);
+  a.pre = static_cast<uint16_t*>(p.pre);
+  a.out2 = static_cast<uint16_t*>(p.out2);
+  a.act = p.act;
+  a.early = p.b_ready;
+  a.status = p.status;
+  a.wait_ns = launch_wait_limit_ns();
+  a.surplus = launch_unreachable_arrivals();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((N + C::kOutCols - 1) / C::kOutCols), static_cast<unsigned>((M + BT - 1) / BT),
+                     static_cast<unsigned>(S));
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 1;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = static_cast<unsigned>(S);
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+template <int EPI, int MAJOR, bool kFp16>
+cudaError_t launch_split_rows(const DenseProblem& p, int BT, int S, cudaStream_t stream) {
+  if constexpr (MAJOR != kMajorMN) {
+    if (BT == 16) return launch_split_variant<EPI, MAJOR, 16, kFp16>(p, S, stream);
+    if (BT == 32) return launch_split_variant<EPI, MAJOR, 32, kFp16>(p, S, stream);
+  }
+  if (BT <= 64) return launch_split_variant<EPI, MAJOR, 64, kFp16>(p, S, stream);
+  if (BT == 128) return launch_split_variant<EPI, MAJOR, 128, kFp16>(p, S, stream);
+  return launch_split_variant<EPI, MAJOR, 256, kFp16>(p, S, stream);
+}
+
+// Which kernel a problem runs on, and how it is cut.
+struct Plan {
+  bool split;
+  int bt, s;  // rows of a tile, parts of k
+};
+
+template <int EPI, int MAJOR>
+Plan plan_of(const DenseProblem& p, int num_sms) {
+  const int oc = EPI == kDenseGate ? 128 : 256;
+  const int64_t pair_tiles = ((p.M + 255) / 256) * ((p.N + oc - 1) / oc);
+  Plan r{};
+  r.split = p.K > 0 && (p.M <= 256 || pair_tiles < 60);
+  if (!r.split) return r;
+  r.bt = MAJOR == kMajorMN ? 64 : 16;
+  while (r.bt < 256 && r.bt < p.M) r.bt *= 2;
+  const int so = EPI == kDenseGate ? 64 : 128;
+  const int64_t tiles = ((p.M + r.bt - 1) / r.bt) * ((p.N + so - 1) / so);
+  const int64_t nk = (p.K + 63) / 64;
+  const int64_t room = r.bt <= 64 ? 2 * num_sms : num_sms;
+  r.s = 1;
+  while (r.s < 8 && tiles * r.s * 2 <= room && r.s * 2 <= nk) r.s *= 2;
+  return r;
+}
+
+template <int EPI, int MAJOR>
+cudaError_t launch_kind(const DenseProblem& p, int num_sms, cudaStream_t stream) {
+  const Plan plan = plan_of<EPI, MAJOR>(p, num_sms);
+  if (plan.split)
+    return p.fp16 ? launch_split_rows<EPI, MAJOR, true>(p, plan.bt, plan.s, stream)
+                  : launch_split_rows<EPI, MAJOR, false>(p, plan.bt, plan.s, stream);
+  return p.fp16 ? launch_variant<EPI, MAJOR, 256, true>(p, num_sms, stream)
+                : launch_variant<EPI, MAJOR, 256, false>(p, num_sms, stream);
+}
+
+}  // namespace dense
+}  // namespace moe
