@@ -407,72 +407,91 @@ def moe_layer_fp8(logits, x, wq: Fp8Experts, k, block_m, act, topk_ids, topk_wei
 
 # ------------------------------------------------- dense operators -------
 
-def _rows(fn, name, t, T, cols, like):
-    """(pointer, row stride) of a [T, cols] matrix of like's type and device
-    whose rows are contiguous; None -> (None, 0)."""
+# These calls are short on the smallest shapes, so their checks are too: one
+# comparison per tensor, with the reason worked out only when it fails.
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(index):
+    """Current stream of a device as an integer handle."""
+    if _raw_stream is not None:
+        return _raw_stream(index)
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+def _refuse(fn, name, t, shape, dtype, index):
+    want = f"{fn}: {name} must be a {list(shape)} {dtype} tensor on cuda:{index}"
+    raise ValueError(f"{want} (rows contiguous), got {list(t.shape)} {t.dtype} on {t.device}, strides {t.stride()}")
+
+
+def _rows(fn, name, t, T, cols, dtype, index):
+    """(pointer, row stride) of a [T, cols] matrix whose rows are contiguous;
+    None -> (None, 0)."""
     if t is None:
         return None, 0
-    if t.dim() != 2 or t.shape[0] != T or t.shape[1] != cols:
-        raise ValueError(f"{fn}: {name} must be [{T}, {cols}], got {list(t.shape)}")
-    if t.dtype != like.dtype or t.device != like.device:
-        raise ValueError(f"{fn}: {name} must be {like.dtype} on {like.device}")
-    if cols > 1 and t.stride(1) != 1:
-        raise ValueError(f"{fn}: {name}'s rows must be contiguous")
+    if t.shape != (T, cols) or t.dtype is not dtype or t.get_device() != index or (t.stride(1) != 1 and cols > 1):
+        _refuse(fn, name, t, (T, cols), dtype, index)
     return t.data_ptr(), t.stride(0) if T > 1 else max(cols, 8)
 
 
-def _whole(fn, name, t, shape, like):
-    """Pointer of a contiguous tensor of the given shape, like's type and
-    device; None -> None."""
+def _whole(fn, name, t, shape, dtype, index):
+    """Pointer of a contiguous tensor of the given shape; None -> None."""
     if t is None:
         return None
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{fn}: {name} must be a contiguous {list(shape)} tensor, got {list(t.shape)}")
-    if t.dtype != like.dtype or t.device != like.device:
-        raise ValueError(f"{fn}: {name} must be {like.dtype} on {like.device}")
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+        _refuse(fn, name, t, shape, dtype, index)
     return t.data_ptr()
 
 
 def _dense_args(fn, x, w, dev_status):
-    if x.dim() != 2 or w.dim() != 2:
-        raise ValueError(f"{fn}: expected 2-D tensors")
-    if not x.is_cuda:
+    """(dtype, dtype code, device index, status pointer) of a call."""
+    index = x.get_device()
+    if index < 0:
         raise ValueError("expected a CUDA tensor")
-    if x.dtype not in (torch.bfloat16, torch.float16):
-        raise ValueError(f"{fn}: expected bfloat16 or float16 tensors")
-    return _DTYPES[x.dtype], _status(fn, dev_status, x.device)
-
-
-def _status(fn, dev_status, device):
+    dtype = x.dtype
+    if (dtype is not torch.bfloat16 and dtype is not torch.float16) or x.dim() != 2 or w.dim() != 2:
+        raise ValueError(f"{fn}: expected 2-D bfloat16 or float16 tensors")
     if dev_status is None:
-        return None
-    if dev_status.dtype != torch.int32 or dev_status.numel() < 1 or dev_status.device != device:
-        raise ValueError(f"{fn}: dev_status must be an int32 tensor on {device}")
-    return dev_status.data_ptr()
+        return dtype, _DTYPES[dtype], index, None
+    if dev_status.dtype is not torch.int32 or dev_status.get_device() != index or dev_status.numel() < 1:
+        raise ValueError(f"{fn}: dev_status must be an int32 tensor on cuda:{index}")
+    return dtype, _DTYPES[dtype], index, dev_status.data_ptr()
 
 
-def _ws(fn, ws, device):
+def _ws(fn, ws, index):
     if ws is None:
         return None, 0
-    if ws.device != device or not ws.is_contiguous():
-        raise ValueError(f"{fn}: ws must be a contiguous tensor on {device}")
+    if ws.get_device() != index or not ws.is_contiguous():
+        raise ValueError(f"{fn}: ws must be a contiguous tensor on cuda:{index}")
     return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _call(fn, index, *args):
+    """Calls the library on the current stream of the device (the last
+    argument) with that device current."""
+    f = getattr(_lib or load_library(), fn)
+    if torch.cuda.current_device() == index:
+        code = f(*args, _stream_of(index))
+    else:
+        with torch.cuda.device(index):
+            code = f(*args, _stream_of(index))
+    if code != 0:
+        raise MoEError(fn, code)
 
 
 def moe_linear(x, w, out, bias=None, residual=None, act=EPI_NONE, pre=None, dev_status=None):
     """out [T, N] = act(x [T, K] . w [N, K]^T + bias) + residual (out may be
     the residual); pre [T, N], when given, keeps x . w^T + bias."""
     fn = "moe_linear"
-    dt, status = _dense_args(fn, x, w, dev_status)
+    dtype, dt, dev, status = _dense_args(fn, x, w, dev_status)
     (T, K), N = x.shape, w.shape[0]
-    px, ldx = _rows(fn, "x", x, T, K, x)
-    pr, ldr = _rows(fn, "residual", residual, T, N, x)
-    po, ldo = _rows(fn, "out", out, T, N, x)
-    with torch.cuda.device(x.device):
-        code = load_library().moe_linear(
-            px, ldx, T, K, _whole(fn, "w", w, (N, K), x), N, _whole(fn, "bias", bias, (N,), x), pr, ldr, act, dt,
-            _whole(fn, "pre", pre, (T, N), x), po, ldo, status, _stream(x.device))
-    _check(fn, code)
+    px, ldx = _rows(fn, "x", x, T, K, dtype, dev)
+    pr, ldr = _rows(fn, "residual", residual, T, N, dtype, dev)
+    po, ldo = _rows(fn, "out", out, T, N, dtype, dev)
+    _call(fn, dev, px, ldx, T, K, _whole(fn, "w", w, (N, K), dtype, dev), N,
+          _whole(fn, "bias", bias, (N,), dtype, dev), pr, ldr, act, dt, _whole(fn, "pre", pre, (T, N), dtype, dev),
+          po, ldo, status)
 
 
 def moe_linear_backward_workspace_size(T, K, N, act, has_bias) -> int:
@@ -485,19 +504,16 @@ def moe_linear_backward(x, w, dout, dx=None, dw=None, dbias=None, act=EPI_NONE, 
     dbias = column sums of dz, with dz = dout * act'(pre); those left None
     are not computed."""
     fn = "moe_linear_backward"
-    dt, status = _dense_args(fn, x, w, dev_status)
+    dtype, dt, dev, status = _dense_args(fn, x, w, dev_status)
     (T, K), N = x.shape, w.shape[0]
-    px, ldx = _rows(fn, "x", x, T, K, x)
-    pd, ldd = _rows(fn, "dout", dout, T, N, x)
-    pr, lddr = _rows(fn, "dx_residual", dx_residual, T, K, x)
-    pdx, lddx = _rows(fn, "dx", dx, T, K, x)
-    pws, nws = _ws(fn, ws, x.device)
-    with torch.cuda.device(x.device):
-        code = load_library().moe_linear_backward(
-            px, ldx, T, K, _whole(fn, "w", w, (N, K), x), N, act, dt, _whole(fn, "pre", pre, (T, N), x), pd, ldd,
-            pr, lddr, pdx, lddx, _whole(fn, "dw", dw, (N, K), x), _whole(fn, "dbias", dbias, (N,), x), pws, nws,
-            status, _stream(x.device))
-    _check(fn, code)
+    px, ldx = _rows(fn, "x", x, T, K, dtype, dev)
+    pd, ldd = _rows(fn, "dout", dout, T, N, dtype, dev)
+    pr, lddr = _rows(fn, "dx_residual", dx_residual, T, K, dtype, dev)
+    pdx, lddx = _rows(fn, "dx", dx, T, K, dtype, dev)
+    pws, nws = _ws(fn, ws, dev)
+    _call(fn, dev, px, ldx, T, K, _whole(fn, "w", w, (N, K), dtype, dev), N, act, dt,
+          _whole(fn, "pre", pre, (T, N), dtype, dev), pd, ldd, pr, lddr, pdx, lddx,
+          _whole(fn, "dw", dw, (N, K), dtype, dev), _whole(fn, "dbias", dbias, (N,), dtype, dev), pws, nws, status)
 
 
 class LinearBuffers:
@@ -536,16 +552,14 @@ def moe_ffn(x, w13, w2, h, out, act=EPI_SILU, residual=None, pre=None, dev_statu
     = h . w2^T + residual, w13 [2F, d] holding Wg's rows, then Wu's; pre
     [T, 2F], when given, keeps both projections for moe_ffn_backward."""
     fn = "moe_ffn"
-    dt, status = _dense_args(fn, x, w2, dev_status)
+    dtype, dt, dev, status = _dense_args(fn, x, w2, dev_status)
     (T, d), F = x.shape, w2.shape[1]
-    px, ldx = _rows(fn, "x", x, T, d, x)
-    pr, ldr = _rows(fn, "residual", residual, T, d, x)
-    po, ldo = _rows(fn, "out", out, T, d, x)
-    with torch.cuda.device(x.device):
-        code = load_library().moe_ffn(
-            px, ldx, T, d, _whole(fn, "w13", w13, (2 * F, d), x), _whole(fn, "w2", w2, (d, F), x), F, act, dt, pr, ldr,
-            _whole(fn, "pre", pre, (T, 2 * F), x), _whole(fn, "h", h, (T, F), x), po, ldo, status, _stream(x.device))
-    _check(fn, code)
+    px, ldx = _rows(fn, "x", x, T, d, dtype, dev)
+    pr, ldr = _rows(fn, "residual", residual, T, d, dtype, dev)
+    po, ldo = _rows(fn, "out", out, T, d, dtype, dev)
+    _call(fn, dev, px, ldx, T, d, _whole(fn, "w13", w13, (2 * F, d), dtype, dev),
+          _whole(fn, "w2", w2, (d, F), dtype, dev), F, act, dt, pr, ldr,
+          _whole(fn, "pre", pre, (T, 2 * F), dtype, dev), _whole(fn, "h", h, (T, F), dtype, dev), po, ldo, status)
 
 
 def moe_ffn_backward_workspace_size(T, d, F) -> int:
@@ -557,20 +571,17 @@ def moe_ffn_backward(x, w13, w2, pre, dout, ws, dx=None, dw13=None, dw2=None, ac
     """Gradients of moe_ffn from the kept pre = [g | u]; those left None are
     not computed."""
     fn = "moe_ffn_backward"
-    dt, status = _dense_args(fn, x, w2, dev_status)
+    dtype, dt, dev, status = _dense_args(fn, x, w2, dev_status)
     (T, d), F = x.shape, w2.shape[1]
-    px, ldx = _rows(fn, "x", x, T, d, x)
-    pd, ldd = _rows(fn, "dout", dout, T, d, x)
-    pr, lddr = _rows(fn, "dx_residual", dx_residual, T, d, x)
-    pdx, lddx = _rows(fn, "dx", dx, T, d, x)
-    pws, nws = _ws(fn, ws, x.device)
-    with torch.cuda.device(x.device):
-        code = load_library().moe_ffn_backward(
-            px, ldx, T, d, _whole(fn, "w13", w13, (2 * F, d), x), _whole(fn, "w2", w2, (d, F), x), F, act, dt,
-            _whole(fn, "pre", pre, (T, 2 * F), x), pd, ldd, pr, lddr, pdx, lddx,
-            _whole(fn, "dw13", dw13, (2 * F, d), x), _whole(fn, "dw2", dw2, (d, F), x), pws, nws, status,
-            _stream(x.device))
-    _check(fn, code)
+    px, ldx = _rows(fn, "x", x, T, d, dtype, dev)
+    pd, ldd = _rows(fn, "dout", dout, T, d, dtype, dev)
+    pr, lddr = _rows(fn, "dx_residual", dx_residual, T, d, dtype, dev)
+    pdx, lddx = _rows(fn, "dx", dx, T, d, dtype, dev)
+    pws, nws = _ws(fn, ws, dev)
+    _call(fn, dev, px, ldx, T, d, _whole(fn, "w13", w13, (2 * F, d), dtype, dev),
+          _whole(fn, "w2", w2, (d, F), dtype, dev), F, act, dt, _whole(fn, "pre", pre, (T, 2 * F), dtype, dev), pd,
+          ldd, pr, lddr, pdx, lddx, _whole(fn, "dw13", dw13, (2 * F, d), dtype, dev),
+          _whole(fn, "dw2", dw2, (d, F), dtype, dev), pws, nws, status)
 
 
 class FFNBuffers:
@@ -629,7 +640,7 @@ class GradClip:
             if not g.is_contiguous() or not o.is_contiguous():
                 raise ValueError("expected a contiguous tensor")
         n = len(grads)
-        self.n, self.device, self._held = n, dev, (grads, outs)
+        self.n, self._held = n, (grads, outs)
         lib = load_library()
         src = (ctypes.c_void_p * n)(*[g.data_ptr() for g in grads])
         dst = (ctypes.c_void_p * n)(*[o.data_ptr() for o in outs])
@@ -641,29 +652,21 @@ class GradClip:
         self.total_norm = torch.zeros((), dtype=torch.float32, device=dev)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
         chunks = ctypes.c_int64(0)
-        with torch.cuda.device(dev):
-            code = lib.moe_grad_plan(src, dst, numel, dtype, n, self.plan.data_ptr(), size, ctypes.byref(chunks),
-                                     _stream(dev))
-        _check("moe_grad_plan", code)
+        self.index = grads[0].get_device()
+        _call("moe_grad_plan", self.index, src, dst, numel, dtype, n, self.plan.data_ptr(), size, ctypes.byref(chunks))
         self.chunks = chunks.value
 
     def norm(self, norm_type=NORM_L2):
         """The global norm (a 0-d fp32 tensor on the device)."""
-        with torch.cuda.device(self.device):
-            code = load_library().moe_grad_norm(
-                self.plan.data_ptr(), self.n, self.chunks, norm_type, self.total_norm.data_ptr(), self.ws.data_ptr(),
-                self.ws.numel(), self.status.data_ptr(), _stream(self.device))
-        _check("moe_grad_norm", code)
+        _call("moe_grad_norm", self.index, self.plan.data_ptr(), self.n, self.chunks, norm_type,
+              self.total_norm.data_ptr(), self.ws.data_ptr(), self.ws.numel(), self.status.data_ptr())
         return self.total_norm
 
     def clip(self, max_norm, norm_type=NORM_L2):
         """Scales the gradients to a global norm of at most max_norm; returns
         the norm before (a 0-d fp32 tensor on the device)."""
-        with torch.cuda.device(self.device):
-            code = load_library().moe_grad_clip(
-                self.plan.data_ptr(), self.n, self.chunks, norm_type, float(max_norm), self.total_norm.data_ptr(),
-                self.ws.data_ptr(), self.ws.numel(), self.status.data_ptr(), _stream(self.device))
-        _check("moe_grad_clip", code)
+        _call("moe_grad_clip", self.index, self.plan.data_ptr(), self.n, self.chunks, norm_type, float(max_norm),
+              self.total_norm.data_ptr(), self.ws.data_ptr(), self.ws.numel(), self.status.data_ptr())
         return self.total_norm
 
 
