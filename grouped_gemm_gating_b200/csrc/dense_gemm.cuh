@@ -18,10 +18,16 @@
 // Operands whose contraction index is not contiguous (dx = dz W reads W by
 // rows of the contraction; dW = dz^T x reads both so) are read MN-major.
 //
-// Two accumulators in tensor memory: the epilogue (eight warps, two per lane
-// quadrant, each on half of the columns) drains one while the MMA fills the
-// other.  Tiles go in groups of kGroupM row tiles, column by column, so the
-// pairs at work share operand rows in L2.
+// Two accumulators in tensor memory: the epilogue (two groups of four warps,
+// each on half of the columns) drains one while the MMA fills the other.
+// Results leave through shared memory in TMA stores of 128 rows x 64 columns,
+// and a residual arrives the same way, ahead of the accumulator and in the
+// buffer its sum is written to: whole lines in both directions, where a
+// thread per row would touch 32 lines with every 16-byte access.
+//
+// Tiles go in groups of kGroupM row tiles, column by column, so the pairs at
+// work share operand rows in L2.  The tiles that do not fill a last round of
+// all pairs are cut into halves of BN / 2 columns when that shortens it.
 //
 // Every mbarrier wait is bounded; on expiry the CTA records
 // MOE_ERR_DEVICE_TIMEOUT and its roles leave their loops; loads and MMAs in
@@ -46,33 +52,39 @@ constexpr int kGroupM = 8;
 
 struct Args {
   CUtensorMap tm_a, tm_b;
-  int64_t M, N, ldr, ldo, ldp;
+  CUtensorMap tm_bh;             // B in boxes of half the rows (half tiles; K-major operands only)
+  CUtensorMap tm_out, tm_pre;    // stores; gate-grad: da and h
+  CUtensorMap tm_res;
+  int64_t M, N, ldr, ldp;
   int nk, n_mt, n_nt;
+  int n_full;                    // whole tiles; the others are cut in two
   const uint16_t* bias;
-  const uint16_t* residual;
-  uint16_t* out;
-  uint16_t* pre;
-  uint16_t* out2;
+  const uint16_t* residual;      // read directly when both it and pre are wanted
+  const uint16_t* pre_in;        // gate-grad: [g | u]
+  int res_tma, keep_pre;
   int act;
   int32_t* status;
   uint64_t wait_ns;
   int tfull_surplus;
 };
 
-template <int EPI, int MAJOR, int BN>
+template <int EPI, int MAJOR>
 struct Cfg {
+  static constexpr int BN = 256;
   static constexpr bool kAMn = MAJOR == kMajorMN;
   static constexpr bool kBMn = MAJOR != kMajorKK;
   static constexpr int kOutCols = EPI == kDenseGate ? BN / 2 : BN;  // output columns of a tile
   static constexpr int kABytes = 128 * 128;                          // 128 M values x 64 K
   static constexpr int kBBytes = BN / 2 * 128;                       // this CTA's half of B
   static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int kStages = BN == 256 ? 6 : 8;
+  static constexpr int kBufs = EPI == kDenseGateGrad ? 3 : 2;        // output buffers of an epilogue group
+  static constexpr int kBufBytes = 128 * 128;                        // 128 rows x 64 columns
+  static constexpr int kStages = EPI == kDenseGateGrad ? 4 : 5;
   static constexpr int kTmemCols = 2 * BN;
   static constexpr int kNumThreads = 320;  // producer, MMA, eight epilogue warps
   static constexpr int kBarrierBytes = 256;
-  static constexpr int kSmemBytes = kStages * kStageBytes + kBarrierBytes + 1024;
-  static_assert((2 * kStages + 5) * 8 + 16 <= kBarrierBytes, "barrier area");
+  static constexpr int kSmemBytes = kStages * kStageBytes + 2 * kBufs * kBufBytes + kBarrierBytes + 1024;
+  static_assert((2 * kStages + 9) * 8 + 16 <= kBarrierBytes, "barrier area");
   static_assert(kSmemBytes <= 232448, "shared memory per block");
 };
 
@@ -118,18 +130,22 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
                     pack2<kFp16>(f[6], f[7]));
 }
 
-template <int EPI, int MAJOR, int BN, bool kFp16>
-__global__ void __launch_bounds__(Cfg<EPI, MAJOR, BN>::kNumThreads, 1)
+template <int EPI, int MAJOR, bool kFp16>
+__global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
     dense_gemm_kernel(const __grid_constant__ Args args) {
-  using C = Cfg<EPI, MAJOR, BN>;
+  using C = Cfg<EPI, MAJOR>;
+  constexpr int BN = C::BN;
   constexpr uint32_t kIdesc = ptx::idesc_16bit_f32(256, BN, kFp16, C::kAMn, C::kBMn);
+  constexpr uint32_t kIdescHalf = ptx::idesc_16bit_f32(256, BN / 2, kFp16, C::kAMn, C::kBMn);
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kStages * C::kStageBytes);
+  uint8_t* bufs = smem + C::kStages * C::kStageBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(bufs + 2 * C::kBufs * C::kBufBytes);
   uint64_t* empty = full + C::kStages;
   uint64_t* tfull = empty + C::kStages;
   uint64_t* tempty = tfull + 2;
-  uint64_t* mma_done = tempty + 2;  // the MMA issuer's last commit (drain before TMEM is freed)
+  uint64_t* res_full = tempty + 2;    // [group][buffer]
+  uint64_t* mma_done = res_full + 4;  // the MMA issuer's last commit (drain before TMEM is freed)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   volatile int* never = reinterpret_cast<volatile int*>(tmem_holder + 2);  // stays 0: drains ignore the abort
@@ -149,6 +165,7 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR, BN>::kNumThreads, 1)
       ptx::mbar_init(&tfull[b], 1 + args.tfull_surplus);
       ptx::mbar_init(&tempty[b], 16);  // even CTA: eight epilogue warps of each CTA
     }
+    for (int i = 0; i < 4; ++i) ptx::mbar_init(&res_full[i], 1);
     ptx::mbar_init(mma_done, 1);
     *abort_flag = 0;
     *never = 0;
@@ -170,15 +187,27 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR, BN>::kNumThreads, 1)
   pdl_launch_dependents();
 
   const int n_mt = args.n_mt, n_nt = args.n_nt, nk = args.nk;
-  const int total_tiles = n_mt * n_nt;
-  auto tile_of = [&](int tile, int* mt, int* nt) {
+  const int units = args.n_full + 2 * (n_mt * n_nt - args.n_full);
+  // Unit u of work: a whole tile (part < 0) or one of a tile's halves.
+  struct Unit {
+    int mt, nt, part;
+  };
+  auto unit_of = [&](int u) {
+    Unit r;
+    int tile = u;
+    r.part = -1;
+    if (u >= args.n_full) {
+      tile = args.n_full + ((u - args.n_full) >> 1);
+      r.part = (u - args.n_full) & 1;
+    }
     const int per_group = kGroupM * n_nt;
     const int g = tile / per_group;
     const int m0 = g * kGroupM;
     const int gm = n_mt - m0 < kGroupM ? n_mt - m0 : kGroupM;
-    const int r = tile - g * per_group;
-    *nt = r / gm;
-    *mt = m0 + (r - *nt * gm);
+    const int i = tile - g * per_group;
+    r.nt = i / gm;
+    r.mt = m0 + (i - r.nt * gm);
+    return r;
   };
   auto fail = [&]() {
     *abort_flag = 1;
@@ -192,11 +221,15 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR, BN>::kNumThreads, 1)
       uint32_t phase = 0;
       bool ok = true;
       int issued = 0;  // stages filled so far
-      for (int tile = pair; ok && tile < total_tiles; tile += n_pairs) {
-        int mt, nt;
-        tile_of(tile, &mt, &nt);
-        const int m0 = mt * 256 + rank * 128;
-        const int n0 = EPI == kDenseGate ? nt * (BN / 2) : nt * BN + rank * (BN / 2);
+      for (int u = pair; ok && u < units; u += n_pairs) {
+        const Unit t = unit_of(u);
+        const bool whole = t.part < 0;
+        const int width = whole ? BN / 2 : BN / 4;  // B rows of this CTA
+        const int m0 = t.mt * 256 + rank * 128;
+        const int n0 = EPI == kDenseGate ? t.nt * (BN / 2) + (t.part > 0 ? width : 0)
+                                         : t.nt * BN + (t.part > 0 ? BN / 2 : 0) + rank * width;
+        const CUtensorMap* tm_b = whole ? &args.tm_b : &args.tm_bh;
+        const uint32_t bytes = 2u * (C::kABytes + (whole ? C::kBBytes : C::kBBytes / 2));
         for (int kb = 0; kb < nk; ++kb) {
           if (!ptx::mbar_wait_cluster_bounded(&empty[stage], phase ^ 1u, abort_flag, args.wait_ns)) {
             fail();
@@ -205,7 +238,7 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR, BN>::kNumThreads, 1)
           }
           uint8_t* sA = smem + stage * C::kStageBytes;
           uint8_t* sB = sA + C::kABytes;
-          if (rank == 0) ptx::mbar_arrive_expect_tx(&full[stage], 2 * C::kStageBytes);
+          if (rank == 0) ptx::mbar_arrive_expect_tx(&full[stage], bytes);
           if constexpr (C::kAMn) {
 #pragma unroll
             for (int j = 0; j < 2; ++j)
@@ -214,13 +247,12 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR, BN>::kNumThreads, 1)
             ptx::tma_load_2d_pair(sA, &args.tm_a, &full[stage], kb * 64, m0);
           }
           if constexpr (EPI == kDenseGate) {
-            ptx::tma_load_3d_pair(sB, &args.tm_b, &full[stage], kb * 64, n0, rank);
+            ptx::tma_load_3d_pair(sB, tm_b, &full[stage], kb * 64, n0, rank);
           } else if constexpr (C::kBMn) {
-#pragma unroll
-            for (int j = 0; j < BN / 128; ++j)
-              ptx::tma_load_2d_pair(sB + j * 8192, &args.tm_b, &full[stage], n0 + 64 * j, kb * 64);
+            ptx::tma_load_2d_pair(sB, &args.tm_b, &full[stage], n0, kb * 64);
+            if (whole) ptx::tma_load_2d_pair(sB + 8192, &args.tm_b, &full[stage], n0 + 64, kb * 64);
           } else {
-            ptx::tma_load_2d_pair(sB, &args.tm_b, &full[stage], kb * 64, n0);
+            ptx::tma_load_2d_pair(sB, tm_b, &full[stage], kb * 64, n0);
           }
           ++issued;
           if (++stage == C::kStages) {
@@ -257,7 +289,8 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR, BN>::kNumThreads, 1)
       int abuf = 0;
       uint32_t aphase = 0;
       bool ok = true;
-      for (int tile = pair; ok && tile < total_tiles; tile += n_pairs) {
+      for (int u = pair; ok && u < units; u += n_pairs) {
+        const uint32_t idesc = u < args.n_full ? kIdesc : kIdescHalf;
         if (!ptx::mbar_wait_cluster_bounded(&tempty[abuf], aphase ^ 1u, abort_flag, args.wait_ns)) {
           fail();
           break;
@@ -279,7 +312,7 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR, BN>::kNumThreads, 1)
                                         : ptx::sw128_kmajor_desc(sA + kk * 32);
             const uint64_t db = C::kBMn ? ptx::sw128_mnmajor_desc(sB + kk * 2048, 8192)
                                         : ptx::sw128_kmajor_desc(sB + kk * 32);
-            ptx::mma_bf16_pair(d_tmem, da, db, kIdesc, (kb | kk) != 0 ? 1u : 0u);
+            ptx::mma_bf16_pair(d_tmem, da, db, idesc, (kb | kk) != 0 ? 1u : 0u);
           }
           ptx::mma_commit_pair(&empty[stage]);
           if (++stage == C::kStages) {
@@ -305,138 +338,246 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR, BN>::kNumThreads, 1)
     // ------------------------------------------------ epilogue (both CTAs, own TMEM half)
     const int q = warp & 3;
     const int half = (warp - 2) >> 2;
+    const int bar = 1 + half;
+    const bool leader = ((warp - 2) & 3) == 0 && lane == 0;  // issues the group's TMA transfers
+    const int r128 = q * 32 + lane;                          // this thread's row of the CTA's 128
+    uint8_t* my_bufs = bufs + half * C::kBufs * C::kBufBytes;
+    auto cell = [&](int b, int j) {  // 16-byte cell j (8 columns) of this thread's row in buffer b
+      return reinterpret_cast<uint4*>(my_bufs + b * C::kBufBytes + r128 * 128 + ((j ^ (r128 & 7)) << 4));
+    };
+    int used = 0;  // buffers of this group whose stores may still be reading
+    auto take = [&](int n) {  // first of n free buffers
+      if (used + n > C::kBufs) {
+        if (leader) ptx::bulk_wait_read();
+        ptx::named_sync(bar, 128);
+        used = 0;
+      }
+      const int b = used;
+      used += n;
+      return b;
+    };
+    auto publish = [&]() {  // what this group wrote is visible to its leader's stores
+      ptx::fence_proxy_async_smem();
+      ptx::named_sync(bar, 128);
+    };
     int abuf = 0;
-    uint32_t aphase = 0;
-    for (int tile = pair; tile < total_tiles; tile += n_pairs) {
-      int mt, nt;
-      tile_of(tile, &mt, &nt);
+    uint32_t aphase = 0, rphase = 0;
+    for (int u = pair; u < units; u += n_pairs) {
+      const Unit t = unit_of(u);
+      const bool whole = t.part < 0;
+      const int m0 = t.mt * 256 + rank * 128;
+      // columns of this group: `chunks` times 64 from `col0` of the output, from `acc0` of the accumulator
+      int col0, acc0, chunks;
+      if constexpr (EPI == kDenseGate) {
+        chunks = whole || half == 0 ? 1 : 0;
+        acc0 = half * 64;
+        col0 = t.nt * 128 + (whole ? acc0 : t.part * 64);
+      } else {
+        chunks = whole ? 2 : 1;
+        acc0 = half * (whole ? 128 : 64);
+        col0 = t.nt * BN + (t.part > 0 ? 128 : 0) + acc0;
+      }
+      while (chunks > 0 && col0 + (chunks - 1) * 64 >= args.N) --chunks;
+      if (m0 >= args.M) chunks = 0;
+      const int64_t row = static_cast<int64_t>(m0) + r128;
+      const bool live = row < args.M;
+      if (leader) {
+        ptx::bulk_wait_read();
+        if (EPI == kDenseLinear && MAJOR != kMajorMN && args.res_tma)
+          for (int c = 0; c < chunks; ++c) {
+            uint64_t* rb = &res_full[half * 2 + c];
+            ptx::mbar_arrive_expect_tx(rb, C::kBufBytes);
+            ptx::tma_load_2d(my_bufs + c * C::kBufBytes, &args.tm_res, rb, col0 + c * 64, m0);
+          }
+      }
+      used = 0;
+      // gate-grad: this row's next 32 columns of g and u, a step ahead
+      uint4 pg[4], pu[4];
+      auto fetch_pre = [&](int col) {
+        const uint16_t* p = args.pre_in + row * args.ldp + col;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (live && col + 8 * i < args.N) {
+            pg[i] = *reinterpret_cast<const uint4*>(p + 8 * i);
+            pu[i] = *reinterpret_cast<const uint4*>(p + args.N + 8 * i);
+          }
+      };
+      if (EPI == kDenseGateGrad && chunks > 0) fetch_pre(col0);
+      bool bad = false;
       if (!ptx::mbar_wait_cluster_bounded(&tfull[abuf], aphase, abort_flag, args.wait_ns)) {
         fail();
+        bad = true;
+      }
+      // a group leaves together, so that none of its threads is left at a barrier
+      if (ptx::named_sync_or(bar, 128, bad)) {
+        if (leader && EPI == kDenseLinear && MAJOR != kMajorMN && args.res_tma)
+          for (int c = 0; c < chunks; ++c) ptx::mbar_wait_bounded(&res_full[half * 2 + c], (rphase >> c) & 1, never, kDrainLimitNs);
         break;
       }
       ptx::tc_fence_after();
-      const uint32_t t_acc = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(abuf * BN);
-      const int64_t row = static_cast<int64_t>(mt) * 256 + rank * 128 + q * 32 + lane;
-      const bool live = row < args.M;
-      const int c_lo = half * (C::kOutCols / 2);
-      const int64_t col0 = static_cast<int64_t>(nt) * C::kOutCols;
+      const uint32_t t_acc =
+          tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(abuf * BN + acc0);
 #pragma unroll 1
-      for (int c0 = c_lo; c0 < c_lo + C::kOutCols / 2; c0 += 32) {
-        const int64_t col = col0 + c0;
-        if (col >= args.N) break;  // uniform across the warp
-        const int groups = args.N - col >= 32 ? 4 : static_cast<int>((args.N - col) >> 3);
+      for (int c = 0; c < chunks; ++c) {
+        const int col = col0 + c * 64;
         if constexpr (EPI == kDenseLinear) {
-          uint32_t a[32];
-          uint4 res[4];
-          const bool has_res = MAJOR != kMajorMN && args.residual != nullptr;
-          if (has_res && live) {
-            const uint4* src = reinterpret_cast<const uint4*>(args.residual + row * args.ldr + col);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (i < groups) res[i] = src[i];
+          const bool keep = MAJOR == kMajorKK && args.keep_pre;
+          const int b = take(keep ? 2 : 1);  // out, pre
+          if (MAJOR != kMajorMN && args.res_tma) {
+            if (!ptx::mbar_wait_bounded(&res_full[half * 2 + c], (rphase >> c) & 1, abort_flag, args.wait_ns)) fail();
+            rphase ^= 1u << c;
           }
-          if (nk > 0) {
-            tmem_ld(t_acc + c0, a);
-            ptx::tmem_wait_ld();
-            pin(a);
-          } else {
+          const bool direct = MAJOR != kMajorMN && args.residual != nullptr && !args.res_tma;
+#pragma unroll 1
+          for (int s = 0; s < 2; ++s) {
+            uint32_t a[32];
+            uint4 res[4], bias[4];
+            const int cs = col + s * 32;
+            if (direct && live) {
+              const uint4* src = reinterpret_cast<const uint4*>(args.residual + row * args.ldr + cs);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) a[j] = 0u;
-          }
-          with_act(MAJOR == kMajorKK ? args.act : MOE_EPI_NONE, [&](auto act) {
+              for (int i = 0; i < 4; ++i)
+                if (cs + 8 * i < args.N) res[i] = src[i];
+            }
+            if (MAJOR == kMajorKK && args.bias != nullptr) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if (live && i < groups) {
+              for (int i = 0; i < 4; ++i)
+                if (cs + 8 * i < args.N) bias[i] = *reinterpret_cast<const uint4*>(args.bias + cs + 8 * i);
+            }
+            if (nk > 0) {
+              tmem_ld(t_acc + c * 64 + s * 32, a);
+              ptx::tmem_wait_ld();
+              pin(a);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) a[j] = 0u;
+            }
+            with_act(MAJOR == kMajorKK ? args.act : MOE_EPI_NONE, [&](auto act) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
                 float v[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(a[8 * i + j]);
                 if constexpr (MAJOR == kMajorKK) {
                   if (args.bias != nullptr) {
-                    float b[8];
-                    unpack8<kFp16>(*reinterpret_cast<const uint4*>(args.bias + col + 8 * i), b);
+                    float bv[8];
+                    unpack8<kFp16>(bias[i], bv);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] += b[j];
+                    for (int j = 0; j < 8; ++j) v[j] += bv[j];
                   }
-                  if (args.pre != nullptr)
-                    *reinterpret_cast<uint4*>(args.pre + row * args.ldp + col + 8 * i) = pack8<kFp16>(v);
+                  if (keep) *cell(b + 1, s * 4 + i) = pack8<kFp16>(v);
 #pragma unroll
                   for (int j = 0; j < 8; ++j) v[j] = act_value(v[j], decltype(act)::value);
                 }
-                if (has_res) {
+                if (MAJOR != kMajorMN && args.residual != nullptr) {
                   float r[8];
-                  unpack8<kFp16>(res[i], r);
+                  unpack8<kFp16>(direct ? res[i] : *cell(b, s * 4 + i), r);
 #pragma unroll
                   for (int j = 0; j < 8; ++j) v[j] += r[j];
                 }
-                *reinterpret_cast<uint4*>(args.out + row * args.ldo + col + 8 * i) = pack8<kFp16>(v);
+                *cell(b, s * 4 + i) = pack8<kFp16>(v);
               }
-            }
-          });
-        } else if constexpr (EPI == kDenseGate) {
-          uint32_t g[32], u[32];
-          tmem_ld(t_acc + c0, g);
-          tmem_ld(t_acc + BN / 2 + c0, u);
-          ptx::tmem_wait_ld();
-          pin(g);
-          pin(u);
-          with_act(args.act, [&](auto act) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if (live && i < groups) {
-                float gv[8], uv[8], h[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                  gv[j] = __uint_as_float(g[8 * i + j]);
-                  uv[j] = __uint_as_float(u[8 * i + j]);
-                  h[j] = act_value(gv[j], decltype(act)::value) * uv[j];
-                }
-                if (args.pre != nullptr) {
-                  uint16_t* p = args.pre + row * args.ldp + col + 8 * i;
-                  *reinterpret_cast<uint4*>(p) = pack8<kFp16>(gv);
-                  *reinterpret_cast<uint4*>(p + args.N) = pack8<kFp16>(uv);
-                }
-                *reinterpret_cast<uint4*>(args.out + row * args.ldo + col + 8 * i) = pack8<kFp16>(h);
-              }
-            }
-          });
-        } else {
-          uint32_t a[32];
-          uint4 pg[4], pu[4];
-          if (live) {
-            const uint16_t* p = args.pre + row * args.ldp + col;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (i < groups) {
-                pg[i] = *reinterpret_cast<const uint4*>(p + 8 * i);
-                pu[i] = *reinterpret_cast<const uint4*>(p + args.N + 8 * i);
-              }
+            });
           }
-          tmem_ld(t_acc + c0, a);
-          ptx::tmem_wait_ld();
-          pin(a);
-          with_act(args.act, [&](auto act) {
+          publish();
+          if (leader) {
+            ptx::tma_store_2d(&args.tm_out, my_bufs + b * C::kBufBytes, col, m0);
+            if (keep) ptx::tma_store_2d(&args.tm_pre, my_bufs + (b + 1) * C::kBufBytes, col, m0);
+            ptx::bulk_commit();
+          }
+        } else if constexpr (EPI == kDenseGate) {
+          const int u_off = whole ? 128 : 64;
+          // first [g | u] as they are, when kept, then h from a second look at the sums
+          for (int step = args.keep_pre ? 0 : 1; step < 2; ++step) {
+            const int b = take(step == 0 ? 2 : 1);
+#pragma unroll 1
+            for (int s = 0; s < 2; ++s) {
+              uint32_t g[32], up[32];
+              tmem_ld(t_acc + s * 32, g);
+              tmem_ld(t_acc + u_off + s * 32, up);
+              ptx::tmem_wait_ld();
+              pin(g);
+              pin(up);
+              if (step == 0) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  float v[8], w[8];
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) {
+                    v[j] = __uint_as_float(g[8 * i + j]);
+                    w[j] = __uint_as_float(up[8 * i + j]);
+                  }
+                  *cell(b, s * 4 + i) = pack8<kFp16>(v);
+                  *cell(b + 1, s * 4 + i) = pack8<kFp16>(w);
+                }
+              } else {
+                with_act(args.act, [&](auto act) {
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    float h[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                      h[j] = act_value(__uint_as_float(g[8 * i + j]), decltype(act)::value) *
+                             __uint_as_float(up[8 * i + j]);
+                    *cell(b, s * 4 + i) = pack8<kFp16>(h);
+                  }
+                });
+              }
+            }
+            publish();
+            if (leader) {
+              if (step == 0) {
+                ptx::tma_store_3d(&args.tm_pre, my_bufs + b * C::kBufBytes, col, 0, m0);
+                ptx::tma_store_3d(&args.tm_pre, my_bufs + (b + 1) * C::kBufBytes, col, 1, m0);
+              } else {
+                ptx::tma_store_2d(&args.tm_out, my_bufs + b * C::kBufBytes, col, m0);
+              }
+              ptx::bulk_commit();
+            }
+          }
+        } else {
+          const int b = take(3);  // dg, du, h
+#pragma unroll 1
+          for (int s = 0; s < 2; ++s) {
+            uint32_t a[32];
+            uint4 g8[4], u8[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              if (live && i < groups) {
-                float g[8], u[8], h[8], dg[8], du[8];
-                unpack8<kFp16>(pg[i], g);
-                unpack8<kFp16>(pu[i], u);
+              g8[i] = pg[i];
+              u8[i] = pu[i];
+            }
+            if (s == 0 || c + 1 < chunks) fetch_pre(col + (s + 1) * 32);
+            tmem_ld(t_acc + c * 64 + s * 32, a);
+            ptx::tmem_wait_ld();
+            pin(a);
+            with_act(args.act, [&](auto act) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                float g[8], up[8], h[8], dg[8], du[8];
+                unpack8<kFp16>(g8[i], g);
+                unpack8<kFp16>(u8[i], up);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                   const float dh = __uint_as_float(a[8 * i + j]);
                   float slope;
                   const float v = act_value_slope(g[j], decltype(act)::value, &slope);
-                  h[j] = v * u[j];
-                  dg[j] = dh * u[j] * slope;
+                  h[j] = v * up[j];
+                  dg[j] = dh * up[j] * slope;
                   du[j] = dh * v;
                 }
-                uint16_t* p = args.out + row * args.ldo + col + 8 * i;
-                *reinterpret_cast<uint4*>(p) = pack8<kFp16>(dg);
-                *reinterpret_cast<uint4*>(p + args.N) = pack8<kFp16>(du);
-                *reinterpret_cast<uint4*>(args.out2 + row * args.N + col + 8 * i) = pack8<kFp16>(h);
+                *cell(b, s * 4 + i) = pack8<kFp16>(dg);
+                *cell(b + 1, s * 4 + i) = pack8<kFp16>(du);
+                *cell(b + 2, s * 4 + i) = pack8<kFp16>(h);
               }
-            }
-          });
+            });
+          }
+          publish();
+          if (leader) {
+            ptx::tma_store_3d(&args.tm_out, my_bufs + b * C::kBufBytes, col, 0, m0);
+            ptx::tma_store_3d(&args.tm_out, my_bufs + (b + 1) * C::kBufBytes, col, 1, m0);
+            ptx::tma_store_2d(&args.tm_pre, my_bufs + (b + 2) * C::kBufBytes, col, m0);
+            ptx::bulk_commit();
+          }
         }
       }
       ptx::tc_fence_before();
@@ -447,6 +588,7 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR, BN>::kNumThreads, 1)
         aphase ^= 1u;
       }
     }
+    if (leader) ptx::bulk_wait();
   }
 
   __syncwarp();
@@ -475,60 +617,82 @@ cudaError_t allow_smem(Kernel kern, int bytes, std::atomic<bool>* done) {
   return cudaSuccess;
 }
 
-template <int EPI, int MAJOR, int BN, bool kFp16>
-cudaError_t launch_variant(const DenseProblem& p, int num_sms, cudaStream_t stream) {
-  using C = Cfg<EPI, MAJOR, BN>;
-  auto kern = dense_gemm_kernel<EPI, MAJOR, BN, kFp16>;
+// 2-D map of a row-major [rows, cols] matrix, or 3-D of [rows, 2, cols] halves.
+inline bool encode_rows(CUtensorMap* m, bool fp16, const void* p, uint64_t rows, uint64_t cols, uint64_t ld,
+                        uint32_t box_cols, uint32_t box_rows) {
+  const uint64_t dims[2] = {cols, rows}, st[1] = {ld * 2};
+  const uint32_t box[2] = {box_cols, box_rows};
+  return encode_16bit(m, fp16, p, 2, dims, st, box);
+}
+inline bool encode_halves(CUtensorMap* m, bool fp16, const void* p, uint64_t rows, uint64_t cols, uint64_t ld,
+                          uint32_t box_rows) {
+  const uint64_t dims[3] = {cols, 2, rows}, st[2] = {cols * 2, ld * 2};
+  const uint32_t box[3] = {64, 1, box_rows};
+  return encode_16bit(m, fp16, p, 3, dims, st, box);
+}
+
+// B's rows in two parts of N each (Wg, Wu).
+inline bool encode_parts(CUtensorMap* m, bool fp16, const void* p, uint64_t K, uint64_t N, uint64_t ld,
+                         uint32_t box_rows) {
+  const uint64_t dims[3] = {K, N, 2}, st[2] = {ld * 2, ld * 2 * N};
+  const uint32_t box[3] = {64, box_rows, 1};
+  return encode_16bit(m, fp16, p, 3, dims, st, box);
+}
+
+template <int EPI, int MAJOR, bool kFp16>
+cudaError_t launch_pair(const DenseProblem& p, int num_sms, cudaStream_t stream) {
+  using C = Cfg<EPI, MAJOR>;
+  auto kern = dense_gemm_kernel<EPI, MAJOR, kFp16>;
   static std::atomic<bool> attr_done[64];
   cudaError_t err = allow_smem(kern, C::kSmemBytes, attr_done);
   if (err != cudaSuccess) return err;
   Args a = {};
-  const uint64_t M = p.M, N = p.N, K = p.K;
-  // With nothing to contract no load is issued; the maps then describe one row.
-  const uint64_t Kd = K > 0 ? K : 8;
-  bool ok;
-  if (C::kAMn) {
-    const uint64_t dims[2] = {M, Kd}, st[1] = {static_cast<uint64_t>(p.lda) * 2};
-    const uint32_t box[2] = {64, 64};
-    ok = encode_16bit(&a.tm_a, kFp16, p.a, 2, dims, st, box);
-  } else {
-    const uint64_t dims[2] = {Kd, M}, st[1] = {static_cast<uint64_t>(p.lda) * 2};
-    const uint32_t box[2] = {64, 128};
-    ok = encode_16bit(&a.tm_a, kFp16, p.a, 2, dims, st, box);
-  }
+  const uint64_t M = p.M, N = p.N;
+  const uint64_t K = p.K > 0 ? p.K : 8;  // with nothing to contract no load is issued
+  bool ok = C::kAMn ? encode_rows(&a.tm_a, kFp16, p.a, K, M, p.lda, 64, 64)
+                    : encode_rows(&a.tm_a, kFp16, p.a, M, K, p.lda, 64, 128);
   if (EPI == kDenseGate) {
-    const uint64_t dims[3] = {Kd, N, 2}, st[2] = {static_cast<uint64_t>(p.ldb) * 2, static_cast<uint64_t>(p.ldb) * 2 * N};
-    const uint32_t box[3] = {64, BN / 2, 1};
-    ok = ok && encode_16bit(&a.tm_b, kFp16, p.b, 3, dims, st, box);
+    ok = ok && encode_parts(&a.tm_b, kFp16, p.b, K, N, p.ldb, 128) && encode_parts(&a.tm_bh, kFp16, p.b, K, N, p.ldb, 64);
   } else if (C::kBMn) {
-    const uint64_t dims[2] = {N, Kd}, st[1] = {static_cast<uint64_t>(p.ldb) * 2};
-    const uint32_t box[2] = {64, 64};
-    ok = ok && encode_16bit(&a.tm_b, kFp16, p.b, 2, dims, st, box);
+    ok = ok && encode_rows(&a.tm_b, kFp16, p.b, K, N, p.ldb, 64, 64);
+    a.tm_bh = a.tm_b;
   } else {
-    const uint64_t dims[2] = {Kd, N}, st[1] = {static_cast<uint64_t>(p.ldb) * 2};
-    const uint32_t box[2] = {64, BN / 2};
-    ok = ok && encode_16bit(&a.tm_b, kFp16, p.b, 2, dims, st, box);
+    ok = ok && encode_rows(&a.tm_b, kFp16, p.b, N, K, p.ldb, 64, 128) &&
+         encode_rows(&a.tm_bh, kFp16, p.b, N, K, p.ldb, 64, 64);
   }
+  if (EPI == kDenseGateGrad) {
+    ok = ok && encode_halves(&a.tm_out, kFp16, p.out, M, N, p.ldo, 128) &&
+         encode_rows(&a.tm_pre, kFp16, p.out2, M, N, N, 64, 128);
+    a.pre_in = static_cast<const uint16_t*>(p.pre);
+  } else {
+    ok = ok && encode_rows(&a.tm_out, kFp16, p.out, M, N, p.ldo, 64, 128);
+    a.keep_pre = p.pre != nullptr;
+    if (p.pre != nullptr)
+      ok = ok && (EPI == kDenseGate ? encode_halves(&a.tm_pre, kFp16, p.pre, M, N, p.ldp, 128)
+                                    : encode_rows(&a.tm_pre, kFp16, p.pre, M, N, p.ldp, 64, 128));
+  }
+  a.residual = static_cast<const uint16_t*>(p.residual);
+  a.res_tma = p.residual != nullptr && p.pre == nullptr;  // with pre, both buffers are outputs
+  if (a.res_tma) ok = ok && encode_rows(&a.tm_res, kFp16, p.residual, M, N, p.ldr, 64, 128);
   if (!ok) return cudaErrorInvalidValue;
   a.M = p.M;
   a.N = p.N;
   a.ldr = p.ldr;
-  a.ldo = p.ldo;
   a.ldp = p.ldp;
   a.nk = static_cast<int>((p.K + 63) / 64);
   a.n_mt = static_cast<int>((p.M + 255) / 256);
   a.n_nt = static_cast<int>((p.N + C::kOutCols - 1) / C::kOutCols);
   a.bias = static_cast<const uint16_t*>(p.bias);
-  a.residual = static_cast<const uint16_t*>(p.residual);
-  a.out = static_cast<uint16_t*>(p.out);
-  a.pre = static_cast<uint16_t*>(p.pre);
-  a.out2 = static_cast<uint16_t*>(p.out2);
   a.act = p.act;
   a.status = p.status;
   a.wait_ns = launch_wait_limit_ns();
   a.tfull_surplus = launch_unreachable_arrivals();
   const int64_t tiles = static_cast<int64_t>(a.n_mt) * a.n_nt;
-  const int pairs = static_cast<int>(tiles < num_sms / 2 ? tiles : num_sms / 2);
+  const int64_t most = num_sms / 2;
+  const int64_t rest = tiles % most;  // halves shorten the last round when they fit into one
+  a.n_full = static_cast<int>(2 * rest <= most ? tiles - rest : tiles);
+  const int64_t units = a.n_full + 2 * (tiles - a.n_full);
+  const int pairs = static_cast<int>(units < most ? units : most);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * pairs);
   cfg.blockDim = dim3(C::kNumThreads);

@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(SplitCfg<EPI, MAJOR, BT>::kThreads)
   const int items = static_cast<int>(live) * ng;
   if (*abort_flag == 0) {
     with_act(EPI == kDenseLinear && MAJOR != kMajorKK ? MOE_EPI_NONE : args.act, [&](auto act) {
-      constexpr int kAct = decltype(act)::value;
+      [[maybe_unused]] constexpr int kAct = decltype(act)::value;
       for (int i = threadIdx.x; i < items; i += C::kThreads) {
         const int t = i / ng;
         const int c = (g0 + i - t * ng) * 4;
@@ -340,29 +340,14 @@ cudaError_t launch_split_variant(const DenseProblem& p, int S, cudaStream_t stre
   if (err != cudaSuccess) return err;
   SplitArgs a = {};
   const uint64_t M = p.M, N = p.N, K = p.K;
-  bool ok;
-  if (C::kRMn) {
-    const uint64_t dims[2] = {M, K}, st[1] = {static_cast<uint64_t>(p.lda) * 2};
-    const uint32_t box[2] = {64, 64};
-    ok = encode_16bit(&a.tm_r, kFp16, p.a, 2, dims, st, box);
-  } else {
-    const uint64_t dims[2] = {K, M}, st[1] = {static_cast<uint64_t>(p.lda) * 2};
-    const uint32_t box[2] = {64, BT};
-    ok = encode_16bit(&a.tm_r, kFp16, p.a, 2, dims, st, box);
-  }
-  if (EPI == kDenseGate) {
-    const uint64_t dims[3] = {K, N, 2}, st[2] = {static_cast<uint64_t>(p.ldb) * 2, static_cast<uint64_t>(p.ldb) * 2 * N};
-    const uint32_t box[3] = {64, 64, 1};
-    ok = ok && encode_16bit(&a.tm_c, kFp16, p.b, 3, dims, st, box);
-  } else if (C::kCMn) {
-    const uint64_t dims[2] = {N, K}, st[1] = {static_cast<uint64_t>(p.ldb) * 2};
-    const uint32_t box[2] = {64, 64};
-    ok = ok && encode_16bit(&a.tm_c, kFp16, p.b, 2, dims, st, box);
-  } else {
-    const uint64_t dims[2] = {K, N}, st[1] = {static_cast<uint64_t>(p.ldb) * 2};
-    const uint32_t box[2] = {64, 128};
-    ok = ok && encode_16bit(&a.tm_c, kFp16, p.b, 2, dims, st, box);
-  }
+  bool ok = C::kRMn ? encode_rows(&a.tm_r, kFp16, p.a, K, M, p.lda, 64, 64)
+                    : encode_rows(&a.tm_r, kFp16, p.a, M, K, p.lda, 64, BT);
+  if (EPI == kDenseGate)
+    ok = ok && encode_parts(&a.tm_c, kFp16, p.b, K, N, p.ldb, 64);
+  else if (C::kCMn)
+    ok = ok && encode_rows(&a.tm_c, kFp16, p.b, K, N, p.ldb, 64, 64);
+  else
+    ok = ok && encode_rows(&a.tm_c, kFp16, p.b, N, K, p.ldb, 64, 128);
   if (!ok) return cudaErrorInvalidValue;
   a.M = p.M;
   a.N = p.N;
@@ -439,8 +424,8 @@ cudaError_t launch_kind(const DenseProblem& p, int num_sms, cudaStream_t stream)
   if (plan.split)
     return p.fp16 ? launch_split_rows<EPI, MAJOR, true>(p, plan.bt, plan.s, stream)
                   : launch_split_rows<EPI, MAJOR, false>(p, plan.bt, plan.s, stream);
-  return p.fp16 ? launch_variant<EPI, MAJOR, 256, true>(p, num_sms, stream)
-                : launch_variant<EPI, MAJOR, 256, false>(p, num_sms, stream);
+  return p.fp16 ? launch_pair<EPI, MAJOR, true>(p, num_sms, stream)
+                : launch_pair<EPI, MAJOR, false>(p, num_sms, stream);
 }
 
 }  // namespace dense
