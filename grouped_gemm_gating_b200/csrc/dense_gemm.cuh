@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
       };
       if (EPI == kDenseGateGrad && chunks > 0) fetch_pre(col0);
       bool bad = false;
-      if (!ptx::mbar_wait_cluster_bounded(&tfull[abuf], aphase, abort_flag, args.wait_ns)) {
+      if (lane == 0 && !ptx::mbar_wait_cluster_bounded(&tfull[abuf], aphase, abort_flag, args.wait_ns)) {
         fail();
         bad = true;
       }
