@@ -216,7 +216,9 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------ TMA producer (both CTAs)
-    if (lane == 0) {
+    if (ptx::elect_one()) {
+      const uint32_t smem0 = ptx::smem_u32(smem);
+      const uint32_t full0 = ptx::leader_addr(full);
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
@@ -236,23 +238,24 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
             ok = false;
             break;
           }
-          uint8_t* sA = smem + stage * C::kStageBytes;
-          uint8_t* sB = sA + C::kABytes;
+          const uint32_t sA = smem0 + stage * C::kStageBytes;
+          const uint32_t sB = sA + C::kABytes;
+          const uint32_t bar = full0 + stage * 8;
           if (rank == 0) ptx::mbar_arrive_expect_tx(&full[stage], bytes);
           if constexpr (C::kAMn) {
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-              ptx::tma_load_2d_pair(sA + j * 8192, &args.tm_a, &full[stage], m0 + 64 * j, kb * 64);
+              ptx::tma_load_2d_pair_at(sA + j * 8192, &args.tm_a, bar, m0 + 64 * j, kb * 64);
           } else {
-            ptx::tma_load_2d_pair(sA, &args.tm_a, &full[stage], kb * 64, m0);
+            ptx::tma_load_2d_pair_at(sA, &args.tm_a, bar, kb * 64, m0);
           }
           if constexpr (EPI == kDenseGate) {
-            ptx::tma_load_3d_pair(sB, tm_b, &full[stage], kb * 64, n0, rank);
+            ptx::tma_load_3d_pair_at(sB, tm_b, bar, kb * 64, n0, rank);
           } else if constexpr (C::kBMn) {
-            ptx::tma_load_2d_pair(sB, &args.tm_b, &full[stage], n0, kb * 64);
-            if (whole) ptx::tma_load_2d_pair(sB + 8192, &args.tm_b, &full[stage], n0 + 64, kb * 64);
+            ptx::tma_load_2d_pair_at(sB, &args.tm_b, bar, n0, kb * 64);
+            if (whole) ptx::tma_load_2d_pair_at(sB + 8192, &args.tm_b, bar, n0 + 64, kb * 64);
           } else {
-            ptx::tma_load_2d_pair(sB, tm_b, &full[stage], kb * 64, n0);
+            ptx::tma_load_2d_pair_at(sB, tm_b, bar, kb * 64, n0);
           }
           ++issued;
           if (++stage == C::kStages) {
@@ -283,7 +286,12 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------ MMA issuer (even CTA)
-    if (lane == 0 && rank == 0) {
+    if (rank == 0 && ptx::elect_one()) {
+      const uint32_t smem0 = ptx::smem_u32(smem);
+      const uint64_t desc_a = C::kAMn ? ptx::sw128_mnmajor_desc(smem0, 8192) : ptx::sw128_kmajor_desc(smem0);
+      const uint64_t desc_b = C::kBMn ? ptx::sw128_mnmajor_desc(smem0 + C::kABytes, 8192)
+                                      : ptx::sw128_kmajor_desc(smem0 + C::kABytes);
+      constexpr int kStepA = (C::kAMn ? 2048 : 32) >> 4, kStepB = (C::kBMn ? 2048 : 32) >> 4;  // 16 K further
       int stage = 0;
       uint32_t phase = 0;
       int abuf = 0;
@@ -304,16 +312,11 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
             break;
           }
           ptx::tc_fence_after();
-          const uint32_t sA = ptx::smem_u32(smem + stage * C::kStageBytes);
-          const uint32_t sB = sA + C::kABytes;
+          const uint32_t st = static_cast<uint32_t>(stage * C::kStageBytes) >> 4;
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const uint64_t da = C::kAMn ? ptx::sw128_mnmajor_desc(sA + kk * 2048, 8192)
-                                        : ptx::sw128_kmajor_desc(sA + kk * 32);
-            const uint64_t db = C::kBMn ? ptx::sw128_mnmajor_desc(sB + kk * 2048, 8192)
-                                        : ptx::sw128_kmajor_desc(sB + kk * 32);
-            ptx::mma_bf16_pair(d_tmem, da, db, idesc, (kb | kk) != 0 ? 1u : 0u);
-          }
+          for (int kk = 0; kk < 4; ++kk)
+            ptx::mma_bf16_pair(d_tmem, desc_a + (st + kk * kStepA), desc_b + (st + kk * kStepB), idesc,
+                               (kb | kk) != 0 ? 1u : 0u);
           ptx::mma_commit_pair(&empty[stage]);
           if (++stage == C::kStages) {
             stage = 0;
@@ -331,7 +334,7 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
       // arrives on both CTAs' mma_done
       ptx::mma_commit_pair(mma_done);
       if (!ptx::mbar_wait_bounded(mma_done, 0u, never, kDrainLimitNs)) fail();
-    } else if (lane == 0) {
+    } else if (rank != 0 && lane == 0) {
       if (!ptx::mbar_wait_cluster_bounded(mma_done, 0u, never, kDrainLimitNs)) fail();
     }
   } else {

@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(SplitCfg<EPI, MAJOR, BT>::kThreads)
   };
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (ptx::elect_one()) {
       // ---------------------------------------------- TMA producer
       auto load_c = [&](int stage, int kb) {
         uint8_t* sC = smem + stage * C::kStageBytes;
@@ -193,8 +193,13 @@ __global__ void __launch_bounds__(SplitCfg<EPI, MAJOR, BT>::kThreads)
         ptx::mbar_wait_bounded(&full[i % C::kStages], (i / C::kStages) & 1, never, kDrainLimitNs);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (ptx::elect_one()) {
       // ---------------------------------------------- MMA issuer
+      const uint32_t smem0 = ptx::smem_u32(smem);
+      const uint64_t desc_c = C::kCMn ? ptx::sw128_mnmajor_desc(smem0, 8192) : ptx::sw128_kmajor_desc(smem0);
+      const uint64_t desc_r = C::kRMn ? ptx::sw128_mnmajor_desc(smem0 + C::kCBytes, 8192)
+                                      : ptx::sw128_kmajor_desc(smem0 + C::kCBytes);
+      constexpr int kStepC = (C::kCMn ? 2048 : 32) >> 4, kStepR = (C::kRMn ? 2048 : 32) >> 4;  // 16 K further
       for (int i = 0; i < kb1 - kb0; ++i) {
         const int st = i % C::kStages;
         if (!ptx::mbar_wait_bounded(&full[st], (i / C::kStages) & 1, abort_flag, args.wait_ns)) {
@@ -202,16 +207,11 @@ __global__ void __launch_bounds__(SplitCfg<EPI, MAJOR, BT>::kThreads)
           break;
         }
         ptx::tc_fence_after();
-        const uint32_t sC = ptx::smem_u32(smem + st * C::kStageBytes);
-        const uint32_t sR = sC + C::kCBytes;
+        const uint32_t off = static_cast<uint32_t>(st * C::kStageBytes) >> 4;
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          const uint64_t dc = C::kCMn ? ptx::sw128_mnmajor_desc(sC + kk * 2048, 8192)
-                                      : ptx::sw128_kmajor_desc(sC + kk * 32);
-          const uint64_t dr = C::kRMn ? ptx::sw128_mnmajor_desc(sR + kk * 2048, 8192)
-                                      : ptx::sw128_kmajor_desc(sR + kk * 32);
-          ptx::mma_bf16(tmem_base, dc, dr, kIdesc, (i | kk) != 0 ? 1u : 0u);
-        }
+        for (int kk = 0; kk < 4; ++kk)
+          ptx::mma_bf16(tmem_base, desc_c + (off + kk * kStepC), desc_r + (off + kk * kStepR), kIdesc,
+                        (i | kk) != 0 ? 1u : 0u);
         ptx::mma_commit(&empty[st]);
       }
       ptx::mma_commit(done);
