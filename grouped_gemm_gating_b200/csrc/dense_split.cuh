@@ -253,80 +253,129 @@ __global__ void __launch_bounds__(SplitCfg<EPI, MAJOR, BT>::kThreads)
   }
 
   // ---- sums over the parts and the epilogue, four columns at a time; this
-  // CTA takes groups [g0, g1) of the tile's columns
+  // CTA takes an S-th of the tile's columns.  Steps of four items a thread,
+  // all their loads before their arithmetic.
   constexpr int kGroups = C::kOutCols / 4;
-  const int g0 = kGroups * rank / S, ng = kGroups * (rank + 1) / S - g0;
-  const int64_t live = args.M - row0 < BT ? args.M - row0 : BT;
-  const uint32_t part_addr = ptx::smem_u32(part);
-  auto sum_at = [&](int t, int c, float (&v)[4]) {
-    const uint32_t off = part_addr + static_cast<uint32_t>(t * C::kPartStride + c) * 4;
-    v[0] = v[1] = v[2] = v[3] = 0.0f;
-    for (int s = 0; s < S; ++s) {
-      const float4 p = ld_cluster_f4(map_rank(off, s));
-      v[0] += p.x;
-      v[1] += p.y;
-      v[2] += p.z;
-      v[3] += p.w;
-    }
-  };
-  const int items = static_cast<int>(live) * ng;
+  const int ng = kGroups / S;  // powers of two
+  const int shift = __ffs(ng) - 1;
+  const int live = static_cast<int>(args.M - row0 < BT ? args.M - row0 : BT);
+  const int items = live * ng;
   if (*abort_flag == 0) {
-    with_act(EPI == kDenseLinear && MAJOR != kMajorKK ? MOE_EPI_NONE : args.act, [&](auto act) {
-      [[maybe_unused]] constexpr int kAct = decltype(act)::value;
-      for (int i = threadIdx.x; i < items; i += C::kThreads) {
-        const int t = i / ng;
-        const int c = (g0 + i - t * ng) * 4;
-        const int64_t row = row0 + t, col = col0 + c;
-        if (col >= args.N) continue;
-        float v[4];
-        sum_at(t, c, v);
-        if constexpr (EPI == kDenseLinear) {
-          if constexpr (MAJOR == kMajorKK) {
-            if (args.bias != nullptr) {
-              float b[4];
-              unpack4<kFp16>(*reinterpret_cast<const uint2*>(args.bias + col), b);
+    auto run = [&](auto parts) {
+      constexpr int kS = decltype(parts)::value;
+      const uint32_t part_addr = ptx::smem_u32(part);
+      uint32_t base[kS];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) v[j] += b[j];
-            }
-            if (args.pre != nullptr) store4<kFp16>(args.pre + row * args.ldp + col, v);
+      for (int s = 0; s < kS; ++s) base[s] = kS == 1 ? part_addr : map_rank(part_addr, s);
+      auto sum_at = [&](int t, int c, float (&v)[4]) {
+        const uint32_t off = static_cast<uint32_t>(t * C::kPartStride + c) * 4;
+        float4 p[kS];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = act_value(v[j], kAct);
-          }
-          if (MAJOR != kMajorMN && args.residual != nullptr) {
-            float r[4];
-            unpack4<kFp16>(*reinterpret_cast<const uint2*>(args.residual + row * args.ldr + col), r);
+        for (int s = 0; s < kS; ++s)
+          p[s] = kS == 1 ? *reinterpret_cast<const float4*>(part + t * C::kPartStride + c) : ld_cluster_f4(base[s] + off);
+        v[0] = p[0].x;
+        v[1] = p[0].y;
+        v[2] = p[0].z;
+        v[3] = p[0].w;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] += r[j];
-          }
-          store4<kFp16>(args.out + row * args.ldo + col, v);
-        } else if constexpr (EPI == kDenseGate) {
-          float u[4], h[4];
-          sum_at(t, c + 64, u);
-          if (args.pre != nullptr) {
-            store4<kFp16>(args.pre + row * args.ldp + col, v);
-            store4<kFp16>(args.pre + row * args.ldp + args.N + col, u);
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) h[j] = act_value(v[j], kAct) * u[j];
-          store4<kFp16>(args.out + row * args.ldo + col, h);
-        } else {
-          float g[4], u[4], dg[4], du[4], h[4];
-          unpack4<kFp16>(*reinterpret_cast<const uint2*>(args.pre + row * args.ldp + col), g);
-          unpack4<kFp16>(*reinterpret_cast<const uint2*>(args.pre + row * args.ldp + args.N + col), u);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float slope;
-            const float a = act_value_slope(g[j], kAct, &slope);
-            h[j] = a * u[j];
-            dg[j] = v[j] * u[j] * slope;
-            du[j] = v[j] * a;
-          }
-          store4<kFp16>(args.out + row * args.ldo + col, dg);
-          store4<kFp16>(args.out + row * args.ldo + args.N + col, du);
-          store4<kFp16>(args.out2 + row * args.N + col, h);
+        for (int s = 1; s < kS; ++s) {
+          v[0] += p[s].x;
+          v[1] += p[s].y;
+          v[2] += p[s].z;
+          v[3] += p[s].w;
         }
+      };
+      constexpr int kU = 4;
+      for (int i0 = threadIdx.x; i0 < items; i0 += kU * C::kThreads) {
+        float v[kU][4], w[kU][4];
+        uint2 x0[kU], x1[kU];  // residual or g; bias or u
+        bool on[kU];
+        int64_t rows[kU], cols[kU];
+#pragma unroll
+        for (int k = 0; k < kU; ++k) {
+          const int i = i0 + k * C::kThreads;
+          const int t = i >> shift;
+          const int c = (rank * ng + (i & (ng - 1))) * 4;
+          rows[k] = row0 + t;
+          cols[k] = col0 + c;
+          on[k] = i < items && cols[k] < args.N;
+          if (!on[k]) continue;
+          if constexpr (EPI == kDenseLinear) {
+            if (MAJOR != kMajorMN && args.residual != nullptr)
+              x0[k] = *reinterpret_cast<const uint2*>(args.residual + rows[k] * args.ldr + cols[k]);
+            if (MAJOR == kMajorKK && args.bias != nullptr) x1[k] = *reinterpret_cast<const uint2*>(args.bias + cols[k]);
+          } else if constexpr (EPI == kDenseGateGrad) {
+            const uint16_t* p = args.pre + rows[k] * args.ldp + cols[k];
+            x0[k] = *reinterpret_cast<const uint2*>(p);
+            x1[k] = *reinterpret_cast<const uint2*>(p + args.N);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kU; ++k) {
+          if (!on[k]) continue;
+          const int t = static_cast<int>(rows[k] - row0), c = static_cast<int>(cols[k] - col0);
+          sum_at(t, c, v[k]);
+          if (EPI == kDenseGate) sum_at(t, c + 64, w[k]);
+        }
+        with_act(EPI == kDenseLinear && MAJOR != kMajorKK ? MOE_EPI_NONE : args.act, [&](auto act) {
+          [[maybe_unused]] constexpr int kAct = decltype(act)::value;
+#pragma unroll
+          for (int k = 0; k < kU; ++k) {
+            if (!on[k]) continue;
+            const int64_t row = rows[k], col = cols[k];
+            if constexpr (EPI == kDenseLinear) {
+              if constexpr (MAJOR == kMajorKK) {
+                if (args.bias != nullptr) {
+                  float b[4];
+                  unpack4<kFp16>(x1[k], b);
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) v[k][j] += b[j];
+                }
+                if (args.pre != nullptr) store4<kFp16>(args.pre + row * args.ldp + col, v[k]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[k][j] = act_value(v[k][j], kAct);
+              }
+              if (MAJOR != kMajorMN && args.residual != nullptr) {
+                float r[4];
+                unpack4<kFp16>(x0[k], r);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[k][j] += r[j];
+              }
+              store4<kFp16>(args.out + row * args.ldo + col, v[k]);
+            } else if constexpr (EPI == kDenseGate) {
+              if (args.pre != nullptr) {
+                store4<kFp16>(args.pre + row * args.ldp + col, v[k]);
+                store4<kFp16>(args.pre + row * args.ldp + args.N + col, w[k]);
+              }
+#pragma unroll
+              for (int j = 0; j < 4; ++j) v[k][j] = act_value(v[k][j], kAct) * w[k][j];
+              store4<kFp16>(args.out + row * args.ldo + col, v[k]);
+            } else {
+              float g[4], u[4], dg[4], du[4], h[4];
+              unpack4<kFp16>(x0[k], g);
+              unpack4<kFp16>(x1[k], u);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                float slope;
+                const float a = act_value_slope(g[j], kAct, &slope);
+                h[j] = a * u[j];
+                dg[j] = v[k][j] * u[j] * slope;
+                du[j] = v[k][j] * a;
+              }
+              store4<kFp16>(args.out + row * args.ldo + col, dg);
+              store4<kFp16>(args.out + row * args.ldo + args.N + col, du);
+              store4<kFp16>(args.out2 + row * args.N + col, h);
+            }
+          }
+        });
       }
-    });
+    };
+    switch (S) {
+      case 1: run(std::integral_constant<int, 1>{}); break;
+      case 2: run(std::integral_constant<int, 2>{}); break;
+      case 4: run(std::integral_constant<int, 4>{}); break;
+      default: run(std::integral_constant<int, 8>{}); break;
+    }
   }
   if (S > 1) ptx::cluster_sync();  // no CTA leaves while another reads its sums
 }
