@@ -17,7 +17,13 @@ enum DenseEpi : int {
 
 // How the two operands lie in memory: K contiguous (rows of the contraction)
 // or their own index contiguous (MN-major).
-enum DenseMajor : int { kMajorKK = 0, kMajorKN = 1, kMajorMN = 2 };  // A K, B K; A K, B MN; A MN, B MN
+enum DenseMajor : int {
+  kMajorKK = 0,   // A K, B K
+  kMajorKN = 1,   // A K, B MN
+  kMajorMN = 2,   // A MN, B MN
+  kMajorAny = 3   // kernels only: kMajorKN and kMajorMN problems together in one launch
+};
+constexpr int kMaxJobs = 3;  // problems of one launch
 
 // One GEMM: sum[m, n] = sum_k A[m, k] B[n, k], m < M, n < N.  16-bit values
 // (bf16, or fp16 with fp16 = 1), strides in elements.
@@ -41,11 +47,15 @@ struct DenseProblem {
   int b_ready;           // b is not written by the kernel before this one in the stream
   int32_t* status;
 };
-cudaError_t launch_dense_gemm(const DenseProblem& p, int num_sms, cudaStream_t stream, int* launches);
+cudaError_t launch_dense_linear(const DenseProblem& p, int num_sms, cudaStream_t stream);
+cudaError_t launch_dense_gate(const DenseProblem& p, int num_sms, cudaStream_t stream);
+cudaError_t launch_dense_gate_grad(const DenseProblem& p, int num_sms, cudaStream_t stream);
+// Up to kMaxJobs independent kMajorKN / kMajorMN products (gradients: no
+// bias, activation or pre) in one launch.
+cudaError_t launch_dense_grads(const DenseProblem* p, int n, int num_sms, cudaStream_t stream);
 
 // dz = dout * act'(pre) (pre null: dz is dout and is not written) and, with
-// dbias, dbias[n] = sum_t dz[t, n]; partial: kDzMaxBlocks * N floats.
-constexpr int kDzMaxBlocks = 256;
+// dbias, dbias[n] = sum_t dz[t, n].
 struct DzArgs {
   const uint16_t* dout;
   int64_t ldd;
@@ -55,9 +65,8 @@ struct DzArgs {
   int act, fp16;
   uint16_t* dz;         // [T, N]
   uint16_t* dbias;      // [N] or null
-  float* partial;
 };
-cudaError_t launch_dz(const DzArgs& a, int num_sms, cudaStream_t stream, int* launches);
+cudaError_t launch_dz(const DzArgs& a, cudaStream_t stream, int* launches);
 
 // Global norm over many tensors and their scaling (clip.cu).  A plan holds
 // one entry per tensor; tensors are cut into chunks of kClipChunk elements

@@ -3,12 +3,12 @@
 // sequences; include/moe.h holds the contract of every entry point.
 #include <cuda_runtime.h>
 
-#include <cmath>
+#include <algorithm>
 #include <cstdint>
+#include <initializer_list>
 
 #include "../../include/moe.h"
 #include "dense.h"
-#include "dense_gemm.cuh"
 #include "host.h"
 
 using moe::aligned16;
@@ -86,21 +86,41 @@ bool disjoint(std::initializer_list<Mat> outs, std::initializer_list<Mat> ins) {
   return true;
 }
 
-struct LinearWs {
-  size_t dz, partial, total;
-};
-LinearWs linear_ws(int64_t T, int64_t N, moe_epi_act act, int has_bias) {
-  LinearWs w{};
-  const size_t dz = act != MOE_EPI_NONE ? round_up(static_cast<size_t>(T) * N * 2, kWsAlign) : 0;
-  const size_t part = has_bias ? round_up(static_cast<size_t>(moe::kDzMaxBlocks) * N * 4, kWsAlign) : 0;
-  w.partial = dz;
-  w.total = dz + part;
-  if (w.total > 0) w.total += kWsAlign;  // ws is rounded up to kWsAlign
-  return w;
+size_t linear_ws(int64_t T, int64_t N, moe_epi_act act) {  // dz; ws is rounded up to kWsAlign
+  return act == MOE_EPI_NONE ? 0 : round_up(static_cast<size_t>(T) * N * 2, kWsAlign) + kWsAlign;
 }
 
 uint8_t* ws_base(void* ws) {
   return reinterpret_cast<uint8_t*>(round_up(reinterpret_cast<uintptr_t>(ws), kWsAlign));
+}
+
+// A gradient product: out [M, N] = a b over a contraction of K, with a [M, K]
+// and b [K, N] (kMajorKN) or a [K, M] and b [K, N] (kMajorMN).
+DenseProblem gradient(int major, moe_dtype dtype, int64_t M, int64_t N, int64_t K, const uint16_t* a, int64_t lda,
+                      const uint16_t* b, int64_t ldb, uint16_t* out, int64_t ldo, int32_t* status) {
+  DenseProblem p{};
+  p.epi = moe::kDenseLinear;
+  p.major = major;
+  p.fp16 = dtype == MOE_FP16;
+  p.act = MOE_EPI_NONE;
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.a = a;
+  p.lda = lda;
+  p.b = b;
+  p.ldb = ldb;
+  p.out = out;
+  p.ldo = ldo;
+  p.status = status;
+  return p;
+}
+
+// One launch for all of them, the longest contraction first.
+moe_status launch_gradients(DenseProblem* jobs, int n, int sms, cudaStream_t s, int launches) {
+  if (n == 0) return finish(cudaSuccess, launches);
+  std::sort(jobs, jobs + n, [](const DenseProblem& a, const DenseProblem& b) { return a.K > b.K; });
+  return finish(moe::launch_dense_grads(jobs, n, sms, s), launches + 1);
 }
 
 Mat ws_mat(void* ws, size_t bytes) {  // the workspace as one row, for the overlap checks
@@ -154,9 +174,9 @@ moe_status moe_linear(const uint16_t* x, int64_t ldx, int64_t T, int K, const ui
   return finish(moe::launch_dense_linear(p, sms, s), 1);
 }
 
-size_t moe_linear_backward_workspace_size(int64_t T, int K, int N, moe_epi_act act, int has_bias) {
+size_t moe_linear_backward_workspace_size(int64_t T, int K, int N, moe_epi_act act) {
   if (check_size(T, K, N) != MOE_OK || !valid_act(act)) return 0;
-  return linear_ws(T, N, act, has_bias).total;
+  return linear_ws(T, N, act);
 }
 
 moe_status moe_linear_backward(const uint16_t* x, int64_t ldx, int64_t T, int K, const uint16_t* w, int N,
@@ -181,9 +201,9 @@ moe_status moe_linear_backward(const uint16_t* x, int64_t ldx, int64_t T, int K,
   }
   if (dw && (st = check_mat(mdw)) != MOE_OK) return st;
   if (dbias && (st = check_mat(mdb)) != MOE_OK) return st;
-  const LinearWs L = linear_ws(T, N, act, dbias != nullptr);
-  if (T > 0 && L.total > 0 && (ws == nullptr || ws_bytes < L.total)) return MOE_ERR_WORKSPACE;
-  const Mat mws = ws_mat(T > 0 && L.total > 0 ? ws : nullptr, ws_bytes);
+  const size_t need = linear_ws(T, N, act);
+  if (T > 0 && need > 0 && (ws == nullptr || ws_bytes < need)) return MOE_ERR_WORKSPACE;
+  const Mat mws = ws_mat(T > 0 && need > 0 ? ws : nullptr, ws_bytes);
   if (!disjoint({mdx, mdw, mdb, mws}, {mx, mw, md, mp}) || share(mr, mdw) || share(mr, mdb) || share(mr, mws) ||
       (share(mr, mdx) && !same(mr, mdx)))
     return MOE_ERR_INVALID_ARG;
@@ -198,7 +218,6 @@ moe_status moe_linear_backward(const uint16_t* x, int64_t ldx, int64_t T, int K,
   }
   const int sms = num_sms_current_device();
   if (sms <= 0) return MOE_ERR_CUDA;
-  uint8_t* base = ws_base(ws);
   const uint16_t* dz = dout;
   int64_t ldz = ldd;
   if (has_act || dbias) {
@@ -211,52 +230,27 @@ moe_status moe_linear_backward(const uint16_t* x, int64_t ldx, int64_t T, int K,
     a.N = N;
     a.act = act;
     a.fp16 = dtype == MOE_FP16;
-    a.dz = reinterpret_cast<uint16_t*>(base + L.dz);
+    a.dz = has_act ? reinterpret_cast<uint16_t*>(ws_base(ws)) : nullptr;
     a.dbias = dbias;
-    a.partial = reinterpret_cast<float*>(base + L.partial);
-    err = moe::launch_dz(a, sms, s, &launches);
+    err = moe::launch_dz(a, s, &launches);
     if (err != cudaSuccess) return MOE_ERR_CUDA;
     if (has_act) {
       dz = a.dz;
       ldz = N;
     }
   }
-  DenseProblem p{};
-  p.epi = moe::kDenseLinear;
-  p.fp16 = dtype == MOE_FP16;
-  p.act = MOE_EPI_NONE;
-  p.a = dz;
-  p.lda = ldz;
-  p.status = dev_status;
-  p.N = K;
+  DenseProblem jobs[2];
+  int n = 0;
+  auto job = [&](int major, int64_t M, int64_t K2, const uint16_t* b, int64_t ldb, uint16_t* out, int64_t ldo) {
+    jobs[n++] = gradient(major, dtype, M, K, K2, dz, ldz, b, ldb, out, ldo, dev_status);
+  };
   if (dx) {
-    p.major = moe::kMajorKN;
-    p.M = T;
-    p.K = N;
-    p.b = w;
-    p.ldb = K;
-    p.residual = dx_residual;
-    p.ldr = lddr;
-    p.out = dx;
-    p.ldo = lddx;
-    err = moe::launch_dense_dx(p, sms, s);
-    if (err != cudaSuccess) return MOE_ERR_CUDA;
-    ++launches;
+    job(moe::kMajorKN, T, N, w, K, dx, lddx);
+    jobs[0].residual = dx_residual;
+    jobs[0].ldr = lddr;
   }
-  if (dw) {
-    p.major = moe::kMajorMN;
-    p.M = N;
-    p.K = T;
-    p.b = x;
-    p.ldb = ldx;
-    p.residual = nullptr;
-    p.out = dw;
-    p.ldo = K;
-    err = moe::launch_dense_dw(p, sms, s);
-    if (err != cudaSuccess) return MOE_ERR_CUDA;
-    ++launches;
-  }
-  return finish(err, launches);
+  if (dw) job(moe::kMajorMN, N, T, x, ldx, dw, K);
+  return launch_gradients(jobs, n, sms, s, launches);
 }
 
 moe_status moe_ffn(const uint16_t* x, int64_t ldx, int64_t T, int d, const uint16_t* w13, const uint16_t* w2, int F,
@@ -393,57 +387,16 @@ moe_status moe_ffn_backward(const uint16_t* x, int64_t ldx, int64_t T, int d, co
   err = moe::launch_dense_gate_grad(p, sms, s);
   if (err != cudaSuccess) return MOE_ERR_CUDA;
   ++launches;
-  p.epi = moe::kDenseLinear;
-  p.act = MOE_EPI_NONE;
-  p.pre = nullptr;
-  p.out2 = nullptr;
+  DenseProblem jobs[3];
+  int n = 0;
   if (dx) {
-    p.major = moe::kMajorKN;
-    p.M = T;
-    p.N = d;
-    p.K = F2;
-    p.a = da;
-    p.lda = F2;
-    p.b = w13;
-    p.ldb = d;
-    p.residual = dx_residual;
-    p.ldr = lddr;
-    p.out = dx;
-    p.ldo = lddx;
-    err = moe::launch_dense_dx(p, sms, s);
-    if (err != cudaSuccess) return MOE_ERR_CUDA;
-    ++launches;
-    p.residual = nullptr;
+    jobs[n] = gradient(moe::kMajorKN, dtype, T, d, F2, da, F2, w13, d, dx, lddx, dev_status);
+    jobs[n].residual = dx_residual;
+    jobs[n++].ldr = lddr;
   }
-  p.major = moe::kMajorMN;
-  p.K = T;
-  if (dw13) {
-    p.M = F2;
-    p.N = d;
-    p.a = da;
-    p.lda = F2;
-    p.b = x;
-    p.ldb = ldx;
-    p.out = dw13;
-    p.ldo = d;
-    err = moe::launch_dense_dw(p, sms, s);
-    if (err != cudaSuccess) return MOE_ERR_CUDA;
-    ++launches;
-  }
-  if (dw2) {
-    p.M = d;
-    p.N = F;
-    p.a = dout;
-    p.lda = ldd;
-    p.b = h;
-    p.ldb = F;
-    p.out = dw2;
-    p.ldo = F;
-    err = moe::launch_dense_dw(p, sms, s);
-    if (err != cudaSuccess) return MOE_ERR_CUDA;
-    ++launches;
-  }
-  return finish(err, launches);
+  if (dw13) jobs[n++] = gradient(moe::kMajorMN, dtype, F2, d, T, da, F2, x, ldx, dw13, d, dev_status);
+  if (dw2) jobs[n++] = gradient(moe::kMajorMN, dtype, d, F, T, dout, ldd, h, F, dw2, F, dev_status);
+  return launch_gradients(jobs, n, sms, s, launches);
 }
 
 size_t moe_grad_plan_size(int n) { return n < 1 || n > (1 << 24) ? 0 : static_cast<size_t>(n) * sizeof(moe::ClipEntry); }

@@ -3,7 +3,7 @@
 namespace moe {
 
 cudaError_t launch_dense_gate_grad(const DenseProblem& p, int num_sms, cudaStream_t stream) {
-  return dense::launch_kind<kDenseGateGrad, kMajorKN>(p, num_sms, stream);
+  return dense::launch_kind<kDenseGateGrad, kMajorKN>(&p, 1, num_sms, stream);
 }
 
 }  // namespace moe

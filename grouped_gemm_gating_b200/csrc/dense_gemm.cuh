@@ -50,18 +50,26 @@ namespace dense {
 constexpr uint64_t kDrainGraceNs = 50000;
 constexpr int kGroupM = 8;
 
-struct Args {
+struct Job {
   CUtensorMap tm_a, tm_b;
   CUtensorMap tm_bh;             // B in boxes of half the rows (half tiles; K-major operands only)
   CUtensorMap tm_out, tm_pre;    // stores; gate-grad: da and h
   CUtensorMap tm_res;
   int64_t M, N, ldr, ldp;
   int nk, n_mt, n_nt;
-  int n_full;                    // whole tiles; the others are cut in two
+  int a_mn, b_mn;                // kMajorAny
   const uint16_t* bias;
   const uint16_t* residual;      // read directly when both it and pre are wanted
   const uint16_t* pre_in;        // gate-grad: [g | u]
   int res_tma, keep_pre;
+};
+
+template <int NJ>
+struct Args {
+  Job job[NJ];
+  int tile0[NJ];                 // first tile of each job; the jobs' tiles are numbered through
+  int n_jobs, n_tiles;
+  int n_full;                    // whole tiles; the others, the last ones, are cut in two
   int act;
   int32_t* status;
   uint64_t wait_ns;
@@ -71,8 +79,7 @@ struct Args {
 template <int EPI, int MAJOR>
 struct Cfg {
   static constexpr int BN = 256;
-  static constexpr bool kAMn = MAJOR == kMajorMN;
-  static constexpr bool kBMn = MAJOR != kMajorKK;
+  static constexpr int kJobs = MAJOR == kMajorAny ? kMaxJobs : 1;
   static constexpr int kOutCols = EPI == kDenseGate ? BN / 2 : BN;  // output columns of a tile
   static constexpr int kABytes = 128 * 128;                          // 128 M values x 64 K
   static constexpr int kBBytes = BN / 2 * 128;                       // this CTA's half of B
@@ -132,11 +139,11 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 
 template <int EPI, int MAJOR, bool kFp16>
 __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
-    dense_gemm_kernel(const __grid_constant__ Args args) {
+    dense_gemm_kernel(const __grid_constant__ Args<Cfg<EPI, MAJOR>::kJobs> args) {
   using C = Cfg<EPI, MAJOR>;
   constexpr int BN = C::BN;
-  constexpr uint32_t kIdesc = ptx::idesc_16bit_f32(256, BN, kFp16, C::kAMn, C::kBMn);
-  constexpr uint32_t kIdescHalf = ptx::idesc_16bit_f32(256, BN / 2, kFp16, C::kAMn, C::kBMn);
+  auto a_mn = [&](const Job& j) { return MAJOR == kMajorAny ? j.a_mn != 0 : MAJOR == kMajorMN; };
+  auto b_mn = [&](const Job& j) { return MAJOR == kMajorAny ? j.b_mn != 0 : MAJOR != kMajorKK; };
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* bufs = smem + C::kStages * C::kStageBytes;
@@ -170,8 +177,8 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
     *abort_flag = 0;
     *never = 0;
     ptx::fence_mbar_init();
-    ptx::prefetch_tmap(&args.tm_a);
-    ptx::prefetch_tmap(&args.tm_b);
+    ptx::prefetch_tmap(&args.job[0].tm_a);
+    ptx::prefetch_tmap(&args.job[0].tm_b);
   }
   if (warp == 1) {
     ptx::tmem_alloc_pair(tmem_holder, C::kTmemCols);
@@ -186,11 +193,13 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
   pdl_wait();
   pdl_launch_dependents();
 
-  const int n_mt = args.n_mt, n_nt = args.n_nt, nk = args.nk;
-  const int units = args.n_full + 2 * (n_mt * n_nt - args.n_full);
-  // Unit u of work: a whole tile (part < 0) or one of a tile's halves.
+  const int units = args.n_full + 2 * (args.n_tiles - args.n_full);
+  // Unit u of work: a whole tile (part < 0) or one of a tile's halves.  The
+  // last round, which may be short, is dealt in the opposite order: the first
+  // pairs then had the larger units of the rounds before.
+  const int last = units - units % n_pairs;
   struct Unit {
-    int mt, nt, part;
+    int job, mt, nt, part;
   };
   auto unit_of = [&](int u) {
     Unit r;
@@ -200,14 +209,27 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
       tile = args.n_full + ((u - args.n_full) >> 1);
       r.part = (u - args.n_full) & 1;
     }
-    const int per_group = kGroupM * n_nt;
+    r.job = 0;
+#pragma unroll
+    for (int j = 1; j < C::kJobs; ++j)
+      if (j < args.n_jobs && tile >= args.tile0[j]) r.job = j;
+    const Job& jb = args.job[r.job];
+    if (C::kJobs > 1) tile -= args.tile0[r.job];
+    const int per_group = kGroupM * jb.n_nt;
     const int g = tile / per_group;
     const int m0 = g * kGroupM;
-    const int gm = n_mt - m0 < kGroupM ? n_mt - m0 : kGroupM;
+    const int gm = jb.n_mt - m0 < kGroupM ? jb.n_mt - m0 : kGroupM;
     const int i = tile - g * per_group;
     r.nt = i / gm;
     r.mt = m0 + (i - r.nt * gm);
     return r;
+  };
+  // This pair's i-th unit, or -1.
+  auto unit_at = [&](int i) {
+    const int u = i * n_pairs + pair;
+    if (u < last) return u;
+    const int v = i * n_pairs + (n_pairs - 1 - pair);
+    return i * n_pairs == last && v < units ? v : -1;
   };
   auto fail = [&]() {
     *abort_flag = 1;
@@ -223,14 +245,16 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
       uint32_t phase = 0;
       bool ok = true;
       int issued = 0;  // stages filled so far
-      for (int u = pair; ok && u < units; u += n_pairs) {
+      for (int it = 0, u; ok && (u = unit_at(it)) >= 0; ++it) {
         const Unit t = unit_of(u);
+        const Job& jb = args.job[t.job];
+        const int nk = jb.nk;
         const bool whole = t.part < 0;
         const int width = whole ? BN / 2 : BN / 4;  // B rows of this CTA
         const int m0 = t.mt * 256 + rank * 128;
         const int n0 = EPI == kDenseGate ? t.nt * (BN / 2) + (t.part > 0 ? width : 0)
                                          : t.nt * BN + (t.part > 0 ? BN / 2 : 0) + rank * width;
-        const CUtensorMap* tm_b = whole ? &args.tm_b : &args.tm_bh;
+        const CUtensorMap* tm_b = whole ? &jb.tm_b : &jb.tm_bh;
         const uint32_t bytes = 2u * (C::kABytes + (whole ? C::kBBytes : C::kBBytes / 2));
         for (int kb = 0; kb < nk; ++kb) {
           if (!ptx::mbar_wait_cluster_bounded(&empty[stage], phase ^ 1u, abort_flag, args.wait_ns)) {
@@ -242,18 +266,18 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
           const uint32_t sB = sA + C::kABytes;
           const uint32_t bar = full0 + stage * 8;
           if (rank == 0) ptx::mbar_arrive_expect_tx(&full[stage], bytes);
-          if constexpr (C::kAMn) {
+          if (a_mn(jb)) {
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-              ptx::tma_load_2d_pair_at(sA + j * 8192, &args.tm_a, bar, m0 + 64 * j, kb * 64);
+              ptx::tma_load_2d_pair_at(sA + j * 8192, &jb.tm_a, bar, m0 + 64 * j, kb * 64);
           } else {
-            ptx::tma_load_2d_pair_at(sA, &args.tm_a, bar, kb * 64, m0);
+            ptx::tma_load_2d_pair_at(sA, &jb.tm_a, bar, kb * 64, m0);
           }
           if constexpr (EPI == kDenseGate) {
             ptx::tma_load_3d_pair_at(sB, tm_b, bar, kb * 64, n0, rank);
-          } else if constexpr (C::kBMn) {
-            ptx::tma_load_2d_pair_at(sB, &args.tm_b, bar, n0, kb * 64);
-            if (whole) ptx::tma_load_2d_pair_at(sB + 8192, &args.tm_b, bar, n0 + 64, kb * 64);
+          } else if (b_mn(jb)) {
+            ptx::tma_load_2d_pair_at(sB, &jb.tm_b, bar, n0, kb * 64);
+            if (whole) ptx::tma_load_2d_pair_at(sB + 8192, &jb.tm_b, bar, n0 + 64, kb * 64);
           } else {
             ptx::tma_load_2d_pair_at(sB, tm_b, bar, kb * 64, n0);
           }
@@ -288,17 +312,20 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
     // ------------------------------------------------ MMA issuer (even CTA)
     if (rank == 0 && ptx::elect_one()) {
       const uint32_t smem0 = ptx::smem_u32(smem);
-      const uint64_t desc_a = C::kAMn ? ptx::sw128_mnmajor_desc(smem0, 8192) : ptx::sw128_kmajor_desc(smem0);
-      const uint64_t desc_b = C::kBMn ? ptx::sw128_mnmajor_desc(smem0 + C::kABytes, 8192)
-                                      : ptx::sw128_kmajor_desc(smem0 + C::kABytes);
-      constexpr int kStepA = (C::kAMn ? 2048 : 32) >> 4, kStepB = (C::kBMn ? 2048 : 32) >> 4;  // 16 K further
       int stage = 0;
       uint32_t phase = 0;
       int abuf = 0;
       uint32_t aphase = 0;
       bool ok = true;
-      for (int u = pair; ok && u < units; u += n_pairs) {
-        const uint32_t idesc = u < args.n_full ? kIdesc : kIdescHalf;
+      for (int it = 0, u; ok && (u = unit_at(it)) >= 0; ++it) {
+        const Job& jb = args.job[unit_of(u).job];
+        const int nk = jb.nk;
+        const bool am = a_mn(jb), bm = b_mn(jb);
+        const uint32_t idesc = ptx::idesc_16bit_f32(256, u < args.n_full ? BN : BN / 2, kFp16, am, bm);
+        const uint64_t desc_a = am ? ptx::sw128_mnmajor_desc(smem0, 8192) : ptx::sw128_kmajor_desc(smem0);
+        const uint64_t desc_b = bm ? ptx::sw128_mnmajor_desc(smem0 + C::kABytes, 8192)
+                                   : ptx::sw128_kmajor_desc(smem0 + C::kABytes);
+        const uint32_t step_a = (am ? 2048 : 32) >> 4, step_b = (bm ? 2048 : 32) >> 4;  // 16 K further
         if (!ptx::mbar_wait_cluster_bounded(&tempty[abuf], aphase ^ 1u, abort_flag, args.wait_ns)) {
           fail();
           break;
@@ -315,7 +342,7 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
           const uint32_t st = static_cast<uint32_t>(stage * C::kStageBytes) >> 4;
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            ptx::mma_bf16_pair(d_tmem, desc_a + (st + kk * kStepA), desc_b + (st + kk * kStepB), idesc,
+            ptx::mma_bf16_pair(d_tmem, desc_a + (st + kk * step_a), desc_b + (st + kk * step_b), idesc,
                                (kb | kk) != 0 ? 1u : 0u);
           ptx::mma_commit_pair(&empty[stage]);
           if (++stage == C::kStages) {
@@ -365,8 +392,9 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
     };
     int abuf = 0;
     uint32_t aphase = 0, rphase = 0;
-    for (int u = pair; u < units; u += n_pairs) {
+    for (int it = 0, u; (u = unit_at(it)) >= 0; ++it) {
       const Unit t = unit_of(u);
+      const Job& jb = args.job[t.job];
       const bool whole = t.part < 0;
       const int m0 = t.mt * 256 + rank * 128;
       // columns of this group: `chunks` times 64 from `col0` of the output, from `acc0` of the accumulator
@@ -380,29 +408,29 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
         acc0 = half * (whole ? 128 : 64);
         col0 = t.nt * BN + (t.part > 0 ? 128 : 0) + acc0;
       }
-      while (chunks > 0 && col0 + (chunks - 1) * 64 >= args.N) --chunks;
-      if (m0 >= args.M) chunks = 0;
+      while (chunks > 0 && col0 + (chunks - 1) * 64 >= jb.N) --chunks;
+      if (m0 >= jb.M) chunks = 0;
       const int64_t row = static_cast<int64_t>(m0) + r128;
-      const bool live = row < args.M;
+      const bool live = row < jb.M;
       if (leader) {
         ptx::bulk_wait_read();
-        if (EPI == kDenseLinear && MAJOR != kMajorMN && args.res_tma)
+        if (EPI == kDenseLinear && jb.res_tma)
           for (int c = 0; c < chunks; ++c) {
             uint64_t* rb = &res_full[half * 2 + c];
             ptx::mbar_arrive_expect_tx(rb, C::kBufBytes);
-            ptx::tma_load_2d(my_bufs + c * C::kBufBytes, &args.tm_res, rb, col0 + c * 64, m0);
+            ptx::tma_load_2d(my_bufs + c * C::kBufBytes, &jb.tm_res, rb, col0 + c * 64, m0);
           }
       }
       used = 0;
       // gate-grad: this row's next 32 columns of g and u, a step ahead
       uint4 pg[4], pu[4];
       auto fetch_pre = [&](int col) {
-        const uint16_t* p = args.pre_in + row * args.ldp + col;
+        const uint16_t* p = jb.pre_in + row * jb.ldp + col;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (live && col + 8 * i < args.N) {
+          if (live && col + 8 * i < jb.N) {
             pg[i] = *reinterpret_cast<const uint4*>(p + 8 * i);
-            pu[i] = *reinterpret_cast<const uint4*>(p + args.N + 8 * i);
+            pu[i] = *reinterpret_cast<const uint4*>(p + jb.N + 8 * i);
           }
       };
       if (EPI == kDenseGateGrad && chunks > 0) fetch_pre(col0);
@@ -413,7 +441,7 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
       }
       // a group leaves together, so that none of its threads is left at a barrier
       if (ptx::named_sync_or(bar, 128, bad)) {
-        if (leader && EPI == kDenseLinear && MAJOR != kMajorMN && args.res_tma)
+        if (leader && EPI == kDenseLinear && jb.res_tma)
           for (int c = 0; c < chunks; ++c) ptx::mbar_wait_bounded(&res_full[half * 2 + c], (rphase >> c) & 1, never, kDrainLimitNs);
         break;
       }
@@ -424,30 +452,30 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
       for (int c = 0; c < chunks; ++c) {
         const int col = col0 + c * 64;
         if constexpr (EPI == kDenseLinear) {
-          const bool keep = MAJOR == kMajorKK && args.keep_pre;
+          const bool keep = MAJOR == kMajorKK && jb.keep_pre;
           const int b = take(keep ? 2 : 1);  // out, pre
-          if (MAJOR != kMajorMN && args.res_tma) {
+          if (jb.res_tma) {
             if (!ptx::mbar_wait_bounded(&res_full[half * 2 + c], (rphase >> c) & 1, abort_flag, args.wait_ns)) fail();
             rphase ^= 1u << c;
           }
-          const bool direct = MAJOR != kMajorMN && args.residual != nullptr && !args.res_tma;
+          const bool direct = jb.residual != nullptr && !jb.res_tma;
 #pragma unroll 1
           for (int s = 0; s < 2; ++s) {
             uint32_t a[32];
             uint4 res[4], bias[4];
             const int cs = col + s * 32;
             if (direct && live) {
-              const uint4* src = reinterpret_cast<const uint4*>(args.residual + row * args.ldr + cs);
+              const uint4* src = reinterpret_cast<const uint4*>(jb.residual + row * jb.ldr + cs);
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                if (cs + 8 * i < args.N) res[i] = src[i];
+                if (cs + 8 * i < jb.N) res[i] = src[i];
             }
-            if (MAJOR == kMajorKK && args.bias != nullptr) {
+            if (MAJOR == kMajorKK && jb.bias != nullptr) {
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                if (cs + 8 * i < args.N) bias[i] = *reinterpret_cast<const uint4*>(args.bias + cs + 8 * i);
+                if (cs + 8 * i < jb.N) bias[i] = *reinterpret_cast<const uint4*>(jb.bias + cs + 8 * i);
             }
-            if (nk > 0) {
+            if (jb.nk > 0) {
               tmem_ld(t_acc + c * 64 + s * 32, a);
               ptx::tmem_wait_ld();
               pin(a);
@@ -462,7 +490,7 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(a[8 * i + j]);
                 if constexpr (MAJOR == kMajorKK) {
-                  if (args.bias != nullptr) {
+                  if (jb.bias != nullptr) {
                     float bv[8];
                     unpack8<kFp16>(bias[i], bv);
 #pragma unroll
@@ -472,7 +500,7 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
 #pragma unroll
                   for (int j = 0; j < 8; ++j) v[j] = act_value(v[j], decltype(act)::value);
                 }
-                if (MAJOR != kMajorMN && args.residual != nullptr) {
+                if (jb.residual != nullptr) {
                   float r[8];
                   unpack8<kFp16>(direct ? res[i] : *cell(b, s * 4 + i), r);
 #pragma unroll
@@ -484,14 +512,14 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
           }
           publish();
           if (leader) {
-            ptx::tma_store_2d(&args.tm_out, my_bufs + b * C::kBufBytes, col, m0);
-            if (keep) ptx::tma_store_2d(&args.tm_pre, my_bufs + (b + 1) * C::kBufBytes, col, m0);
+            ptx::tma_store_2d(&jb.tm_out, my_bufs + b * C::kBufBytes, col, m0);
+            if (keep) ptx::tma_store_2d(&jb.tm_pre, my_bufs + (b + 1) * C::kBufBytes, col, m0);
             ptx::bulk_commit();
           }
         } else if constexpr (EPI == kDenseGate) {
           const int u_off = whole ? 128 : 64;
           // first [g | u] as they are, when kept, then h from a second look at the sums
-          for (int step = args.keep_pre ? 0 : 1; step < 2; ++step) {
+          for (int step = jb.keep_pre ? 0 : 1; step < 2; ++step) {
             const int b = take(step == 0 ? 2 : 1);
 #pragma unroll 1
             for (int s = 0; s < 2; ++s) {
@@ -530,10 +558,10 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
             publish();
             if (leader) {
               if (step == 0) {
-                ptx::tma_store_3d(&args.tm_pre, my_bufs + b * C::kBufBytes, col, 0, m0);
-                ptx::tma_store_3d(&args.tm_pre, my_bufs + (b + 1) * C::kBufBytes, col, 1, m0);
+                ptx::tma_store_3d(&jb.tm_pre, my_bufs + b * C::kBufBytes, col, 0, m0);
+                ptx::tma_store_3d(&jb.tm_pre, my_bufs + (b + 1) * C::kBufBytes, col, 1, m0);
               } else {
-                ptx::tma_store_2d(&args.tm_out, my_bufs + b * C::kBufBytes, col, m0);
+                ptx::tma_store_2d(&jb.tm_out, my_bufs + b * C::kBufBytes, col, m0);
               }
               ptx::bulk_commit();
             }
@@ -576,9 +604,9 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
           }
           publish();
           if (leader) {
-            ptx::tma_store_3d(&args.tm_out, my_bufs + b * C::kBufBytes, col, 0, m0);
-            ptx::tma_store_3d(&args.tm_out, my_bufs + (b + 1) * C::kBufBytes, col, 1, m0);
-            ptx::tma_store_2d(&args.tm_pre, my_bufs + (b + 2) * C::kBufBytes, col, m0);
+            ptx::tma_store_3d(&jb.tm_out, my_bufs + b * C::kBufBytes, col, 0, m0);
+            ptx::tma_store_3d(&jb.tm_out, my_bufs + (b + 1) * C::kBufBytes, col, 1, m0);
+            ptx::tma_store_2d(&jb.tm_pre, my_bufs + (b + 2) * C::kBufBytes, col, m0);
             ptx::bulk_commit();
           }
         }
@@ -643,54 +671,70 @@ inline bool encode_parts(CUtensorMap* m, bool fp16, const void* p, uint64_t K, u
 }
 
 template <int EPI, int MAJOR, bool kFp16>
-cudaError_t launch_pair(const DenseProblem& p, int num_sms, cudaStream_t stream) {
+bool make_job(const DenseProblem& p, Job* a) {
+  using C = Cfg<EPI, MAJOR>;
+  const bool a_mn = p.major == kMajorMN, b_mn = p.major != kMajorKK;
+  const uint64_t M = p.M, N = p.N;
+  const uint64_t K = p.K > 0 ? p.K : 8;  // with nothing to contract no load is issued
+  bool ok = a_mn ? encode_rows(&a->tm_a, kFp16, p.a, K, M, p.lda, 64, 64)
+                 : encode_rows(&a->tm_a, kFp16, p.a, M, K, p.lda, 64, 128);
+  if (EPI == kDenseGate) {
+    ok = ok && encode_parts(&a->tm_b, kFp16, p.b, K, N, p.ldb, 128) &&
+         encode_parts(&a->tm_bh, kFp16, p.b, K, N, p.ldb, 64);
+  } else if (b_mn) {
+    ok = ok && encode_rows(&a->tm_b, kFp16, p.b, K, N, p.ldb, 64, 64);
+    a->tm_bh = a->tm_b;
+  } else {
+    ok = ok && encode_rows(&a->tm_b, kFp16, p.b, N, K, p.ldb, 64, 128) &&
+         encode_rows(&a->tm_bh, kFp16, p.b, N, K, p.ldb, 64, 64);
+  }
+  if (EPI == kDenseGateGrad) {
+    ok = ok && encode_halves(&a->tm_out, kFp16, p.out, M, N, p.ldo, 128) &&
+         encode_rows(&a->tm_pre, kFp16, p.out2, M, N, N, 64, 128);
+    a->pre_in = static_cast<const uint16_t*>(p.pre);
+  } else {
+    ok = ok && encode_rows(&a->tm_out, kFp16, p.out, M, N, p.ldo, 64, 128);
+    a->keep_pre = p.pre != nullptr;
+    if (p.pre != nullptr)
+      ok = ok && (EPI == kDenseGate ? encode_halves(&a->tm_pre, kFp16, p.pre, M, N, p.ldp, 128)
+                                    : encode_rows(&a->tm_pre, kFp16, p.pre, M, N, p.ldp, 64, 128));
+  }
+  a->residual = static_cast<const uint16_t*>(p.residual);
+  a->res_tma = p.residual != nullptr && p.pre == nullptr;  // with pre, both buffers are outputs
+  if (a->res_tma) ok = ok && encode_rows(&a->tm_res, kFp16, p.residual, M, N, p.ldr, 64, 128);
+  a->M = p.M;
+  a->N = p.N;
+  a->ldr = p.ldr;
+  a->ldp = p.ldp;
+  a->a_mn = a_mn;
+  a->b_mn = b_mn;
+  a->nk = static_cast<int>((p.K + 63) / 64);
+  a->n_mt = static_cast<int>((p.M + 255) / 256);
+  a->n_nt = static_cast<int>((p.N + C::kOutCols - 1) / C::kOutCols);
+  a->bias = static_cast<const uint16_t*>(p.bias);
+  return ok;
+}
+
+template <int EPI, int MAJOR, bool kFp16>
+cudaError_t launch_pair(const DenseProblem* p, int n, int num_sms, cudaStream_t stream) {
   using C = Cfg<EPI, MAJOR>;
   auto kern = dense_gemm_kernel<EPI, MAJOR, kFp16>;
   static std::atomic<bool> attr_done[64];
   cudaError_t err = allow_smem(kern, C::kSmemBytes, attr_done);
   if (err != cudaSuccess) return err;
-  Args a = {};
-  const uint64_t M = p.M, N = p.N;
-  const uint64_t K = p.K > 0 ? p.K : 8;  // with nothing to contract no load is issued
-  bool ok = C::kAMn ? encode_rows(&a.tm_a, kFp16, p.a, K, M, p.lda, 64, 64)
-                    : encode_rows(&a.tm_a, kFp16, p.a, M, K, p.lda, 64, 128);
-  if (EPI == kDenseGate) {
-    ok = ok && encode_parts(&a.tm_b, kFp16, p.b, K, N, p.ldb, 128) && encode_parts(&a.tm_bh, kFp16, p.b, K, N, p.ldb, 64);
-  } else if (C::kBMn) {
-    ok = ok && encode_rows(&a.tm_b, kFp16, p.b, K, N, p.ldb, 64, 64);
-    a.tm_bh = a.tm_b;
-  } else {
-    ok = ok && encode_rows(&a.tm_b, kFp16, p.b, N, K, p.ldb, 64, 128) &&
-         encode_rows(&a.tm_bh, kFp16, p.b, N, K, p.ldb, 64, 64);
+  Args<C::kJobs> a = {};
+  int64_t tiles = 0;
+  for (int i = 0; i < n; ++i) {
+    if (!make_job<EPI, MAJOR, kFp16>(p[i], &a.job[i])) return cudaErrorInvalidValue;
+    a.tile0[i] = static_cast<int>(tiles);
+    tiles += static_cast<int64_t>(a.job[i].n_mt) * a.job[i].n_nt;
   }
-  if (EPI == kDenseGateGrad) {
-    ok = ok && encode_halves(&a.tm_out, kFp16, p.out, M, N, p.ldo, 128) &&
-         encode_rows(&a.tm_pre, kFp16, p.out2, M, N, N, 64, 128);
-    a.pre_in = static_cast<const uint16_t*>(p.pre);
-  } else {
-    ok = ok && encode_rows(&a.tm_out, kFp16, p.out, M, N, p.ldo, 64, 128);
-    a.keep_pre = p.pre != nullptr;
-    if (p.pre != nullptr)
-      ok = ok && (EPI == kDenseGate ? encode_halves(&a.tm_pre, kFp16, p.pre, M, N, p.ldp, 128)
-                                    : encode_rows(&a.tm_pre, kFp16, p.pre, M, N, p.ldp, 64, 128));
-  }
-  a.residual = static_cast<const uint16_t*>(p.residual);
-  a.res_tma = p.residual != nullptr && p.pre == nullptr;  // with pre, both buffers are outputs
-  if (a.res_tma) ok = ok && encode_rows(&a.tm_res, kFp16, p.residual, M, N, p.ldr, 64, 128);
-  if (!ok) return cudaErrorInvalidValue;
-  a.M = p.M;
-  a.N = p.N;
-  a.ldr = p.ldr;
-  a.ldp = p.ldp;
-  a.nk = static_cast<int>((p.K + 63) / 64);
-  a.n_mt = static_cast<int>((p.M + 255) / 256);
-  a.n_nt = static_cast<int>((p.N + C::kOutCols - 1) / C::kOutCols);
-  a.bias = static_cast<const uint16_t*>(p.bias);
-  a.act = p.act;
-  a.status = p.status;
+  a.n_jobs = n;
+  a.n_tiles = static_cast<int>(tiles);
+  a.act = p[0].act;
+  a.status = p[0].status;
   a.wait_ns = launch_wait_limit_ns();
   a.tfull_surplus = launch_unreachable_arrivals();
-  const int64_t tiles = static_cast<int64_t>(a.n_mt) * a.n_nt;
   const int64_t most = num_sms / 2;
   const int64_t rest = tiles % most;  // halves shorten the last round when they fit into one
   a.n_full = static_cast<int>(2 * rest <= most ? tiles - rest : tiles);
@@ -714,12 +758,5 @@ cudaError_t launch_pair(const DenseProblem& p, int num_sms, cudaStream_t stream)
 }
 
 }  // namespace dense
-
-// One translation unit per kind.
-cudaError_t launch_dense_linear(const DenseProblem& p, int num_sms, cudaStream_t stream);
-cudaError_t launch_dense_dx(const DenseProblem& p, int num_sms, cudaStream_t stream);
-cudaError_t launch_dense_dw(const DenseProblem& p, int num_sms, cudaStream_t stream);
-cudaError_t launch_dense_gate(const DenseProblem& p, int num_sms, cudaStream_t stream);
-cudaError_t launch_dense_gate_grad(const DenseProblem& p, int num_sms, cudaStream_t stream);
 
 }  // namespace moe

@@ -3,7 +3,7 @@
 namespace moe {
 
 cudaError_t launch_dense_linear(const DenseProblem& p, int num_sms, cudaStream_t stream) {
-  return dense::launch_kind<kDenseLinear, kMajorKK>(p, num_sms, stream);
+  return dense::launch_kind<kDenseLinear, kMajorKK>(&p, 1, num_sms, stream);
 }
 
 }  // namespace moe

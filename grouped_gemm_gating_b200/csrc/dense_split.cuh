@@ -6,7 +6,7 @@
 // by their bytes (or, small enough, by latency), and every SM has to pull.
 // Here a tile is 128 output columns x BT rows, with the roles of the operands
 // swapped: the columns' operand (the weights) is the MMA's M = 128 side, the
-// rows its N = BT side (16 to 256).  A cluster of S CTAs shares one tile,
+// rows its N = BT side (16 to 128).  A cluster of S CTAs shares one tile,
 // each contracting its part of k; the fp32 parts meet in shared memory, every
 // CTA adds the S parts of its share of the columns through distributed shared
 // memory, always in the same order, and applies the epilogue to the sum.  No
@@ -19,15 +19,24 @@
 namespace moe {
 namespace dense {
 
-struct SplitArgs {
+struct SplitJob {
   CUtensorMap tm_c, tm_r;  // the columns' operand, the rows' operand
   int64_t M, N, ldr, ldo, ldp;
-  int nk;
+  int nk, n_ct;            // k-blocks; tiles along the columns
+  int r_mn;                // kMajorAny: the rows' operand is MN-major too
   const uint16_t* bias;
   const uint16_t* residual;
   uint16_t* out;
   uint16_t* pre;
   uint16_t* out2;
+};
+
+template <int NJ>
+struct SplitArgs {
+  SplitJob job[NJ];
+  int tile0[NJ];           // first tile of each job; the jobs' tiles are numbered through
+  int n_jobs;
+  int S;                   // CTAs of a cluster: parts of k
   int act;
   int early;               // columns' operand is not written by the previous kernel of the stream
   int32_t* status;
@@ -38,36 +47,21 @@ struct SplitArgs {
 template <int EPI, int MAJOR, int BT>
 struct SplitCfg {
   static constexpr bool kCMn = MAJOR != kMajorKK;
-  static constexpr bool kRMn = MAJOR == kMajorMN;
+  static constexpr int kJobs = MAJOR == kMajorAny ? kMaxJobs : 1;
   static constexpr int kOutCols = EPI == kDenseGate ? 64 : 128;
   static constexpr int kCBytes = 128 * 128;
   static constexpr int kRBytes = BT * 128;
   static constexpr int kStageBytes = kCBytes + kRBytes;
   // two CTAs on an SM up to 64 rows, one beyond
-  static constexpr int kStages = BT <= 16 ? 6 : BT <= 32 ? 5 : BT <= 64 ? 4 : BT <= 128 ? 6 : 4;
+  static constexpr int kStages = BT <= 16 ? 6 : BT <= 32 ? 5 : BT <= 64 ? 4 : 6;
   static constexpr int kTmemCols = BT < 32 ? 32 : BT;
   static constexpr int kThreads = 256;
   static constexpr int kPartStride = 132;  // floats between two rows' sums of the 128 columns
   static constexpr int kSmemBytes = kStages * kStageBytes + 256 + 1024;
   static_assert(BT * kPartStride * 4 <= kStages * kStageBytes, "sums reuse the stages");
-  static_assert(!kRMn || BT % 64 == 0, "row operand chunks");
+  static_assert(MAJOR != kMajorAny || BT % 64 == 0, "row operand chunks");
   static_assert(kSmemBytes <= 232448, "shared memory per block");
 };
-
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
-
-__device__ __forceinline__ uint32_t map_rank(uint32_t smem_addr, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr), "r"(rank));
-  return r;
-}
 
 template <bool kFp16>
 __device__ __forceinline__ void unpack4(uint2 v, float (&f)[4]) {
@@ -85,9 +79,8 @@ __device__ __forceinline__ void store4(uint16_t* p, const float (&f)[4]) {
 
 template <int EPI, int MAJOR, int BT, bool kFp16>
 __global__ void __launch_bounds__(SplitCfg<EPI, MAJOR, BT>::kThreads)
-    dense_split_kernel(const __grid_constant__ SplitArgs args) {
+    dense_split_kernel(const __grid_constant__ SplitArgs<SplitCfg<EPI, MAJOR, BT>::kJobs> args) {
   using C = SplitCfg<EPI, MAJOR, BT>;
-  constexpr uint32_t kIdesc = ptx::idesc_16bit_f32(128, BT, kFp16, C::kCMn, C::kRMn);
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kStages * C::kStageBytes);
@@ -100,12 +93,20 @@ __global__ void __launch_bounds__(SplitCfg<EPI, MAJOR, BT>::kThreads)
 
   const int warp = threadIdx.x / kWarp;
   const int lane = threadIdx.x % kWarp;
-  const int S = static_cast<int>(gridDim.z);  // CTAs of a cluster: parts of k
-  const int rank = static_cast<int>(blockIdx.z);
-  const int64_t col0 = static_cast<int64_t>(blockIdx.x) * C::kOutCols;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.y) * BT;
-  const int kb0 = static_cast<int>(static_cast<int64_t>(args.nk) * rank / S);
-  const int kb1 = static_cast<int>(static_cast<int64_t>(args.nk) * (rank + 1) / S);
+  const int S = args.S;
+  const int rank = static_cast<int>(blockIdx.x) % S;
+  int tile = static_cast<int>(blockIdx.x) / S;
+  int which = 0;
+#pragma unroll
+  for (int j = 1; j < C::kJobs; ++j)
+    if (j < args.n_jobs && tile >= args.tile0[j]) which = j;
+  const SplitJob& jb = args.job[which];
+  if (C::kJobs > 1) tile -= args.tile0[which];
+  const bool r_mn = MAJOR == kMajorAny && jb.r_mn;
+  const int64_t col0 = static_cast<int64_t>(tile % jb.n_ct) * C::kOutCols;
+  const int64_t row0 = static_cast<int64_t>(tile / jb.n_ct) * BT;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(jb.nk) * rank / S);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(jb.nk) * (rank + 1) / S);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
@@ -117,8 +118,8 @@ __global__ void __launch_bounds__(SplitCfg<EPI, MAJOR, BT>::kThreads)
     *abort_flag = 0;
     *never = 0;
     ptx::fence_mbar_init();
-    ptx::prefetch_tmap(&args.tm_c);
-    ptx::prefetch_tmap(&args.tm_r);
+    ptx::prefetch_tmap(&jb.tm_c);
+    ptx::prefetch_tmap(&jb.tm_r);
   }
   if (warp == 1) {
     ptx::tmem_alloc(tmem_holder, C::kTmemCols);
@@ -139,23 +140,23 @@ __global__ void __launch_bounds__(SplitCfg<EPI, MAJOR, BT>::kThreads)
       auto load_c = [&](int stage, int kb) {
         uint8_t* sC = smem + stage * C::kStageBytes;
         if constexpr (EPI == kDenseGate) {
-          ptx::tma_load_3d(sC, &args.tm_c, &full[stage], kb * 64, static_cast<int>(col0), 0);
-          ptx::tma_load_3d(sC + 8192, &args.tm_c, &full[stage], kb * 64, static_cast<int>(col0), 1);
+          ptx::tma_load_3d(sC, &jb.tm_c, &full[stage], kb * 64, static_cast<int>(col0), 0);
+          ptx::tma_load_3d(sC + 8192, &jb.tm_c, &full[stage], kb * 64, static_cast<int>(col0), 1);
         } else if constexpr (C::kCMn) {
-          ptx::tma_load_2d(sC, &args.tm_c, &full[stage], static_cast<int>(col0), kb * 64);
-          ptx::tma_load_2d(sC + 8192, &args.tm_c, &full[stage], static_cast<int>(col0) + 64, kb * 64);
+          ptx::tma_load_2d(sC, &jb.tm_c, &full[stage], static_cast<int>(col0), kb * 64);
+          ptx::tma_load_2d(sC + 8192, &jb.tm_c, &full[stage], static_cast<int>(col0) + 64, kb * 64);
         } else {
-          ptx::tma_load_2d(sC, &args.tm_c, &full[stage], kb * 64, static_cast<int>(col0));
+          ptx::tma_load_2d(sC, &jb.tm_c, &full[stage], kb * 64, static_cast<int>(col0));
         }
       };
       auto load_r = [&](int stage, int kb) {
         uint8_t* sR = smem + stage * C::kStageBytes + C::kCBytes;
-        if constexpr (C::kRMn) {
+        if (MAJOR == kMajorAny && r_mn) {
 #pragma unroll
           for (int j = 0; j < BT / 64; ++j)
-            ptx::tma_load_2d(sR + j * 8192, &args.tm_r, &full[stage], static_cast<int>(row0) + 64 * j, kb * 64);
+            ptx::tma_load_2d(sR + j * 8192, &jb.tm_r, &full[stage], static_cast<int>(row0) + 64 * j, kb * 64);
         } else {
-          ptx::tma_load_2d(sR, &args.tm_r, &full[stage], kb * 64, static_cast<int>(row0));
+          ptx::tma_load_2d(sR, &jb.tm_r, &full[stage], kb * 64, static_cast<int>(row0));
         }
       };
       const int n = kb1 - kb0;
@@ -197,9 +198,11 @@ __global__ void __launch_bounds__(SplitCfg<EPI, MAJOR, BT>::kThreads)
       // ---------------------------------------------- MMA issuer
       const uint32_t smem0 = ptx::smem_u32(smem);
       const uint64_t desc_c = C::kCMn ? ptx::sw128_mnmajor_desc(smem0, 8192) : ptx::sw128_kmajor_desc(smem0);
-      const uint64_t desc_r = C::kRMn ? ptx::sw128_mnmajor_desc(smem0 + C::kCBytes, 8192)
-                                      : ptx::sw128_kmajor_desc(smem0 + C::kCBytes);
-      constexpr int kStepC = (C::kCMn ? 2048 : 32) >> 4, kStepR = (C::kRMn ? 2048 : 32) >> 4;  // 16 K further
+      const uint64_t desc_r = r_mn ? ptx::sw128_mnmajor_desc(smem0 + C::kCBytes, 8192)
+                                   : ptx::sw128_kmajor_desc(smem0 + C::kCBytes);
+      constexpr uint32_t kStepC = (C::kCMn ? 2048 : 32) >> 4;  // 16 K further
+      const uint32_t step_r = (r_mn ? 2048 : 32) >> 4;
+      const uint32_t idesc = ptx::idesc_16bit_f32(128, BT, kFp16, C::kCMn, r_mn);
       for (int i = 0; i < kb1 - kb0; ++i) {
         const int st = i % C::kStages;
         if (!ptx::mbar_wait_bounded(&full[st], (i / C::kStages) & 1, abort_flag, args.wait_ns)) {
@@ -210,7 +213,7 @@ __global__ void __launch_bounds__(SplitCfg<EPI, MAJOR, BT>::kThreads)
         const uint32_t off = static_cast<uint32_t>(st * C::kStageBytes) >> 4;
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          ptx::mma_bf16(tmem_base, desc_c + (off + kk * kStepC), desc_r + (off + kk * kStepR), kIdesc,
+          ptx::mma_bf16(tmem_base, desc_c + (off + kk * kStepC), desc_r + (off + kk * step_r), idesc,
                         (i | kk) != 0 ? 1u : 0u);
         ptx::mma_commit(&empty[st]);
       }
@@ -225,7 +228,8 @@ __global__ void __launch_bounds__(SplitCfg<EPI, MAJOR, BT>::kThreads)
   __syncthreads();  // the stages are free: every load landed, every MMA read them
   ptx::tc_fence_after();
 
-  // ---- this CTA's sums, [row][128 columns], in place of the stages
+  // ---- this CTA's sums, [row][128 columns], in place of the stages (a job
+  // with fewer k-blocks than parts leaves some CTAs none)
   float* part = reinterpret_cast<float*>(smem);
   {
     const int q = warp & 3;
@@ -241,7 +245,7 @@ __global__ void __launch_bounds__(SplitCfg<EPI, MAJOR, BT>::kThreads)
         ptx::tmem_wait_ld();
         pin(a);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) dst[(c + j) * C::kPartStride] = __uint_as_float(a[j]);
+        for (int j = 0; j < 16; ++j) dst[(c + j) * C::kPartStride] = kb1 > kb0 ? __uint_as_float(a[j]) : 0.0f;
       }
     }
   }
@@ -258,7 +262,7 @@ __global__ void __launch_bounds__(SplitCfg<EPI, MAJOR, BT>::kThreads)
   constexpr int kGroups = C::kOutCols / 4;
   const int ng = kGroups / S;  // powers of two
   const int shift = __ffs(ng) - 1;
-  const int live = static_cast<int>(args.M - row0 < BT ? args.M - row0 : BT);
+  const int live = static_cast<int>(jb.M - row0 < BT ? jb.M - row0 : BT);
   const int items = live * ng;
   if (*abort_flag == 0) {
     auto run = [&](auto parts) {
@@ -266,13 +270,13 @@ __global__ void __launch_bounds__(SplitCfg<EPI, MAJOR, BT>::kThreads)
       const uint32_t part_addr = ptx::smem_u32(part);
       uint32_t base[kS];
 #pragma unroll
-      for (int s = 0; s < kS; ++s) base[s] = kS == 1 ? part_addr : map_rank(part_addr, s);
+      for (int s = 0; s < kS; ++s) base[s] = kS == 1 ? part_addr : ptx::map_rank(part_addr, s);
       auto sum_at = [&](int t, int c, float (&v)[4]) {
         const uint32_t off = static_cast<uint32_t>(t * C::kPartStride + c) * 4;
         float4 p[kS];
 #pragma unroll
         for (int s = 0; s < kS; ++s)
-          p[s] = kS == 1 ? *reinterpret_cast<const float4*>(part + t * C::kPartStride + c) : ld_cluster_f4(base[s] + off);
+          p[s] = kS == 1 ? *reinterpret_cast<const float4*>(part + t * C::kPartStride + c) : ptx::ld_cluster_f4(base[s] + off);
         v[0] = p[0].x;
         v[1] = p[0].y;
         v[2] = p[0].z;
@@ -298,16 +302,16 @@ __global__ void __launch_bounds__(SplitCfg<EPI, MAJOR, BT>::kThreads)
           const int c = (rank * ng + (i & (ng - 1))) * 4;
           rows[k] = row0 + t;
           cols[k] = col0 + c;
-          on[k] = i < items && cols[k] < args.N;
+          on[k] = i < items && cols[k] < jb.N;
           if (!on[k]) continue;
           if constexpr (EPI == kDenseLinear) {
-            if (MAJOR != kMajorMN && args.residual != nullptr)
-              x0[k] = *reinterpret_cast<const uint2*>(args.residual + rows[k] * args.ldr + cols[k]);
-            if (MAJOR == kMajorKK && args.bias != nullptr) x1[k] = *reinterpret_cast<const uint2*>(args.bias + cols[k]);
+            if (jb.residual != nullptr)
+              x0[k] = *reinterpret_cast<const uint2*>(jb.residual + rows[k] * jb.ldr + cols[k]);
+            if (MAJOR == kMajorKK && jb.bias != nullptr) x1[k] = *reinterpret_cast<const uint2*>(jb.bias + cols[k]);
           } else if constexpr (EPI == kDenseGateGrad) {
-            const uint16_t* p = args.pre + rows[k] * args.ldp + cols[k];
+            const uint16_t* p = jb.pre + rows[k] * jb.ldp + cols[k];
             x0[k] = *reinterpret_cast<const uint2*>(p);
-            x1[k] = *reinterpret_cast<const uint2*>(p + args.N);
+            x1[k] = *reinterpret_cast<const uint2*>(p + jb.N);
           }
         }
 #pragma unroll
@@ -325,31 +329,31 @@ __global__ void __launch_bounds__(SplitCfg<EPI, MAJOR, BT>::kThreads)
             const int64_t row = rows[k], col = cols[k];
             if constexpr (EPI == kDenseLinear) {
               if constexpr (MAJOR == kMajorKK) {
-                if (args.bias != nullptr) {
+                if (jb.bias != nullptr) {
                   float b[4];
                   unpack4<kFp16>(x1[k], b);
 #pragma unroll
                   for (int j = 0; j < 4; ++j) v[k][j] += b[j];
                 }
-                if (args.pre != nullptr) store4<kFp16>(args.pre + row * args.ldp + col, v[k]);
+                if (jb.pre != nullptr) store4<kFp16>(jb.pre + row * jb.ldp + col, v[k]);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) v[k][j] = act_value(v[k][j], kAct);
               }
-              if (MAJOR != kMajorMN && args.residual != nullptr) {
+              if (jb.residual != nullptr) {
                 float r[4];
                 unpack4<kFp16>(x0[k], r);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) v[k][j] += r[j];
               }
-              store4<kFp16>(args.out + row * args.ldo + col, v[k]);
+              store4<kFp16>(jb.out + row * jb.ldo + col, v[k]);
             } else if constexpr (EPI == kDenseGate) {
-              if (args.pre != nullptr) {
-                store4<kFp16>(args.pre + row * args.ldp + col, v[k]);
-                store4<kFp16>(args.pre + row * args.ldp + args.N + col, w[k]);
+              if (jb.pre != nullptr) {
+                store4<kFp16>(jb.pre + row * jb.ldp + col, v[k]);
+                store4<kFp16>(jb.pre + row * jb.ldp + jb.N + col, w[k]);
               }
 #pragma unroll
               for (int j = 0; j < 4; ++j) v[k][j] = act_value(v[k][j], kAct) * w[k][j];
-              store4<kFp16>(args.out + row * args.ldo + col, v[k]);
+              store4<kFp16>(jb.out + row * jb.ldo + col, v[k]);
             } else {
               float g[4], u[4], dg[4], du[4], h[4];
               unpack4<kFp16>(x0[k], g);
@@ -362,9 +366,9 @@ __global__ void __launch_bounds__(SplitCfg<EPI, MAJOR, BT>::kThreads)
                 dg[j] = v[k][j] * u[j] * slope;
                 du[j] = v[k][j] * a;
               }
-              store4<kFp16>(args.out + row * args.ldo + col, dg);
-              store4<kFp16>(args.out + row * args.ldo + args.N + col, du);
-              store4<kFp16>(args.out2 + row * args.N + col, h);
+              store4<kFp16>(jb.out + row * jb.ldo + col, dg);
+              store4<kFp16>(jb.out + row * jb.ldo + jb.N + col, du);
+              store4<kFp16>(jb.out2 + row * jb.N + col, h);
             }
           }
         });
@@ -381,42 +385,53 @@ __global__ void __launch_bounds__(SplitCfg<EPI, MAJOR, BT>::kThreads)
 }
 
 template <int EPI, int MAJOR, int BT, bool kFp16>
-cudaError_t launch_split_variant(const DenseProblem& p, int S, cudaStream_t stream) {
+cudaError_t launch_split_variant(const DenseProblem* p, int n, int S, cudaStream_t stream) {
   using C = SplitCfg<EPI, MAJOR, BT>;
   auto kern = dense_split_kernel<EPI, MAJOR, BT, kFp16>;
   static std::atomic<bool> attr_done[64];
   cudaError_t err = allow_smem(kern, C::kSmemBytes, attr_done);
   if (err != cudaSuccess) return err;
-  SplitArgs a = {};
-  const uint64_t M = p.M, N = p.N, K = p.K;
-  bool ok = C::kRMn ? encode_rows(&a.tm_r, kFp16, p.a, K, M, p.lda, 64, 64)
-                    : encode_rows(&a.tm_r, kFp16, p.a, M, K, p.lda, 64, BT);
-  if (EPI == kDenseGate)
-    ok = ok && encode_parts(&a.tm_c, kFp16, p.b, K, N, p.ldb, 64);
-  else if (C::kCMn)
-    ok = ok && encode_rows(&a.tm_c, kFp16, p.b, K, N, p.ldb, 64, 64);
-  else
-    ok = ok && encode_rows(&a.tm_c, kFp16, p.b, N, K, p.ldb, 64, 128);
-  if (!ok) return cudaErrorInvalidValue;
-  a.M = p.M;
-  a.N = p.N;
-  a.ldr = p.ldr;
-  a.ldo = p.ldo;
-  a.ldp = p.ldp;
-  a.nk = static_cast<int>((p.K + 63) / 64);
-  a.bias = static_cast<const uint16_t*>(p.bias);
-  a.residual = static_cast<const uint16_t*>(p.residual);
-  a.out = static_cast<uint16_t*>(p.out);
-  a.pre = static_cast<uint16_t*>(p.pre);
-  a.out2 = static_cast<uint16_t*>(p.out2);
-  a.act = p.act;
-  a.early = p.b_ready;
-  a.status = p.status;
+  SplitArgs<C::kJobs> a = {};
+  int64_t tiles = 0;
+  for (int i = 0; i < n; ++i) {
+    const DenseProblem& q = p[i];
+    SplitJob& j = a.job[i];
+    const uint64_t M = q.M, N = q.N, K = q.K;
+    const bool r_mn = q.major == kMajorMN;
+    bool ok = r_mn ? encode_rows(&j.tm_r, kFp16, q.a, K, M, q.lda, 64, 64)
+                   : encode_rows(&j.tm_r, kFp16, q.a, M, K, q.lda, 64, BT);
+    if (EPI == kDenseGate)
+      ok = ok && encode_parts(&j.tm_c, kFp16, q.b, K, N, q.ldb, 64);
+    else if (C::kCMn)
+      ok = ok && encode_rows(&j.tm_c, kFp16, q.b, K, N, q.ldb, 64, 64);
+    else
+      ok = ok && encode_rows(&j.tm_c, kFp16, q.b, N, K, q.ldb, 64, 128);
+    if (!ok) return cudaErrorInvalidValue;
+    j.M = q.M;
+    j.N = q.N;
+    j.ldr = q.ldr;
+    j.ldo = q.ldo;
+    j.ldp = q.ldp;
+    j.nk = static_cast<int>((q.K + 63) / 64);
+    j.n_ct = static_cast<int>((q.N + C::kOutCols - 1) / C::kOutCols);
+    j.r_mn = r_mn;
+    j.bias = static_cast<const uint16_t*>(q.bias);
+    j.residual = static_cast<const uint16_t*>(q.residual);
+    j.out = static_cast<uint16_t*>(q.out);
+    j.pre = static_cast<uint16_t*>(q.pre);
+    j.out2 = static_cast<uint16_t*>(q.out2);
+    a.tile0[i] = static_cast<int>(tiles);
+    tiles += static_cast<int64_t>(j.n_ct) * ((q.M + BT - 1) / BT);
+  }
+  a.n_jobs = n;
+  a.S = S;
+  a.act = p[0].act;
+  a.early = p[0].b_ready;
+  a.status = p[0].status;
   a.wait_ns = launch_wait_limit_ns();
   a.surplus = launch_unreachable_arrivals();
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((N + C::kOutCols - 1) / C::kOutCols), static_cast<unsigned>((M + BT - 1) / BT),
-                     static_cast<unsigned>(S));
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * S));
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::kSmemBytes;
   cfg.stream = stream;
@@ -424,57 +439,59 @@ cudaError_t launch_split_variant(const DenseProblem& p, int S, cudaStream_t stre
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 1;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(S);
   attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = static_cast<unsigned>(S);
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
 template <int EPI, int MAJOR, bool kFp16>
-cudaError_t launch_split_rows(const DenseProblem& p, int BT, int S, cudaStream_t stream) {
-  if constexpr (MAJOR != kMajorMN) {
-    if (BT == 16) return launch_split_variant<EPI, MAJOR, 16, kFp16>(p, S, stream);
-    if (BT == 32) return launch_split_variant<EPI, MAJOR, 32, kFp16>(p, S, stream);
+cudaError_t launch_split_rows(const DenseProblem* p, int n, int BT, int S, cudaStream_t stream) {
+  if constexpr (MAJOR != kMajorAny) {
+    if (BT == 16) return launch_split_variant<EPI, MAJOR, 16, kFp16>(p, n, S, stream);
+    if (BT == 32) return launch_split_variant<EPI, MAJOR, 32, kFp16>(p, n, S, stream);
   }
-  if (BT <= 64) return launch_split_variant<EPI, MAJOR, 64, kFp16>(p, S, stream);
-  if (BT == 128) return launch_split_variant<EPI, MAJOR, 128, kFp16>(p, S, stream);
-  return launch_split_variant<EPI, MAJOR, 256, kFp16>(p, S, stream);
+  if (BT <= 64) return launch_split_variant<EPI, MAJOR, 64, kFp16>(p, n, S, stream);
+  return launch_split_variant<EPI, MAJOR, 128, kFp16>(p, n, S, stream);
 }
 
-// Which kernel a problem runs on, and how it is cut.
+// Which kernel a launch's problems run on, and how they are cut.
 struct Plan {
   bool split;
   int bt, s;  // rows of a tile, parts of k
 };
 
 template <int EPI, int MAJOR>
-Plan plan_of(const DenseProblem& p, int num_sms) {
-  const int oc = EPI == kDenseGate ? 128 : 256;
-  const int64_t pair_tiles = ((p.M + 255) / 256) * ((p.N + oc - 1) / oc);
+Plan plan_of(const DenseProblem* p, int n, int num_sms) {
+  const int oc = EPI == kDenseGate ? 128 : 256, so = EPI == kDenseGate ? 64 : 128;
+  int64_t pair_tiles = 0, rows = 0, nk = 0;
+  for (int i = 0; i < n; ++i) {
+    pair_tiles += ((p[i].M + 255) / 256) * ((p[i].N + oc - 1) / oc);
+    if (p[i].M > rows) rows = p[i].M;
+    if (p[i].K > nk * 64) nk = (p[i].K + 63) / 64;
+  }
   Plan r{};
-  r.split = p.K > 0 && (p.M <= 256 || pair_tiles < 60);
+  r.split = pair_tiles < 60;
   if (!r.split) return r;
-  r.bt = MAJOR == kMajorMN ? 64 : 16;
-  while (r.bt < 256 && r.bt < p.M) r.bt *= 2;
-  const int so = EPI == kDenseGate ? 64 : 128;
-  const int64_t tiles = ((p.M + r.bt - 1) / r.bt) * ((p.N + so - 1) / so);
-  const int64_t nk = (p.K + 63) / 64;
-  const int64_t room = r.bt <= 64 ? 2 * num_sms : num_sms;
+  r.bt = MAJOR == kMajorAny ? 64 : 16;
+  while (r.bt < 64 && r.bt < rows) r.bt *= 2;
+  int64_t tiles = 0;
+  for (int i = 0; i < n; ++i) tiles += ((p[i].M + r.bt - 1) / r.bt) * ((p[i].N + so - 1) / so);
   r.s = 1;
-  while (r.s < 8 && tiles * r.s * 2 <= room && r.s * 2 <= nk) r.s *= 2;
+  while (r.s < 8 && tiles * r.s * 2 <= 2 * num_sms && r.s * 2 <= nk) r.s *= 2;
   return r;
 }
 
 template <int EPI, int MAJOR>
-cudaError_t launch_kind(const DenseProblem& p, int num_sms, cudaStream_t stream) {
-  const Plan plan = plan_of<EPI, MAJOR>(p, num_sms);
+cudaError_t launch_kind(const DenseProblem* p, int n, int num_sms, cudaStream_t stream) {
+  const Plan plan = plan_of<EPI, MAJOR>(p, n, num_sms);
   if (plan.split)
-    return p.fp16 ? launch_split_rows<EPI, MAJOR, true>(p, plan.bt, plan.s, stream)
-                  : launch_split_rows<EPI, MAJOR, false>(p, plan.bt, plan.s, stream);
-  return p.fp16 ? launch_pair<EPI, MAJOR, true>(p, num_sms, stream)
-                : launch_pair<EPI, MAJOR, false>(p, num_sms, stream);
+    return p->fp16 ? launch_split_rows<EPI, MAJOR, true>(p, n, plan.bt, plan.s, stream)
+                   : launch_split_rows<EPI, MAJOR, false>(p, n, plan.bt, plan.s, stream);
+  return p->fp16 ? launch_pair<EPI, MAJOR, true>(p, n, num_sms, stream)
+                 : launch_pair<EPI, MAJOR, false>(p, n, num_sms, stream);
 }
 
 }  // namespace dense

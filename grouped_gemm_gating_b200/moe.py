@@ -61,7 +61,7 @@ _SIG = {
     "moe_layer_fp8": (_I, [_P, _I, _I, _I, _I, _I, _I, _I, ctypes.c_float, _P, _I, _P, _P, _P, _P, _I, _P, _P, _P,
                            _P, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P, _P]),
     "moe_linear": (_I, [_P, _L, _L, _I, _P, _I, _P, _P, _L, _I, _I, _P, _P, _L, _P, _P]),
-    "moe_linear_backward_workspace_size": (ctypes.c_size_t, [_L, _I, _I, _I, _I]),
+    "moe_linear_backward_workspace_size": (ctypes.c_size_t, [_L, _I, _I, _I]),
     "moe_linear_backward": (_I, [_P, _L, _L, _I, _P, _I, _I, _I, _P, _P, _L, _P, _L, _P, _L, _P, _P, _P,
                                  ctypes.c_size_t, _P, _P]),
     "moe_ffn": (_I, [_P, _L, _L, _I, _P, _P, _I, _I, _I, _P, _L, _P, _P, _P, _L, _P, _P]),
@@ -494,8 +494,8 @@ def moe_linear(x, w, out, bias=None, residual=None, act=EPI_NONE, pre=None, dev_
           po, ldo, status)
 
 
-def moe_linear_backward_workspace_size(T, K, N, act, has_bias) -> int:
-    return int(load_library().moe_linear_backward_workspace_size(T, K, N, act, 1 if has_bias else 0))
+def moe_linear_backward_workspace_size(T, K, N, act) -> int:
+    return int(load_library().moe_linear_backward_workspace_size(T, K, N, act))
 
 
 def moe_linear_backward(x, w, dout, dx=None, dw=None, dbias=None, act=EPI_NONE, pre=None, ws=None, dx_residual=None,
@@ -533,7 +533,7 @@ class LinearBuffers:
             self.dx = torch.empty((T, K), **kw)
             self.dw = torch.empty((N, K), **kw)
             self.dbias = torch.empty(N, **kw) if bias else None
-            n = moe_linear_backward_workspace_size(T, K, N, act, bias)
+            n = moe_linear_backward_workspace_size(T, K, N, act)
             self.ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
 
     def forward(self, x, w, bias=None, residual=None):

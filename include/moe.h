@@ -464,10 +464,9 @@ MOE_API moe_status moe_linear(const uint16_t* x, int64_t ldx, int64_t T, int K, 
                       uint16_t* pre, uint16_t* out, int64_t ldo,
                       int32_t* dev_status, moe_stream_t stream);
 
-/* Bytes of scratch of moe_linear_backward (0 when it needs none, or on
- * invalid arguments): dz [T, N] when there is an activation, and partial
- * sums when dbias is wanted (has_bias). */
-MOE_API size_t moe_linear_backward_workspace_size(int64_t T, int K, int N, moe_epi_act act, int has_bias);
+/* Bytes of scratch of moe_linear_backward: dz [T, N] when there is an
+ * activation (0 when it needs none, or on invalid arguments). */
+MOE_API size_t moe_linear_backward_workspace_size(int64_t T, int K, int N, moe_epi_act act);
 
 /*
  * moe_linear_backward -- with dz = dout * act'(pre):

@@ -146,12 +146,10 @@ def test_ffn_backward_checks(lib):
 
 
 def test_workspace_sizes(lib):
-    assert M.moe_linear_backward_workspace_size(100, 64, 32, M.EPI_NONE, False) == 0
-    n = M.moe_linear_backward_workspace_size(100, 64, 32, M.EPI_SILU, False)
+    assert M.moe_linear_backward_workspace_size(100, 64, 32, M.EPI_NONE) == 0
+    n = M.moe_linear_backward_workspace_size(100, 64, 32, M.EPI_SILU)
     assert 100 * 32 * 2 <= n <= 100 * 32 * 2 + 512
-    n = M.moe_linear_backward_workspace_size(100, 64, 32, M.EPI_NONE, True)
-    assert n >= 32 * 4
-    assert M.moe_linear_backward_workspace_size(100, 60, 32, M.EPI_SILU, True) == 0
+    assert M.moe_linear_backward_workspace_size(100, 60, 32, M.EPI_SILU) == 0
     n = M.moe_ffn_backward_workspace_size(100, 64, 32)
     assert 100 * 3 * 32 * 2 <= n <= 100 * 3 * 32 * 2 + 768
     assert M.moe_ffn_backward_workspace_size(100, 64, 30) == 0

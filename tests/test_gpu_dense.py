@@ -142,7 +142,7 @@ def test_linear_backward(T, K, N, name, bias, res, dtype, pad):
     buf, dx = d.out(T, K)
     dw = torch.full((N, K), 77.0, dtype=dtype, device="cuda")
     db = torch.full((N,), 77.0, dtype=dtype, device="cuda") if bias else None
-    n = M.moe_linear_backward_workspace_size(T, K, N, EPI[name], bias)
+    n = M.moe_linear_backward_workspace_size(T, K, N, EPI[name])
     ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda") if n else None
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
     M.moe_linear_backward(x, w, dout, dx, dw, db, EPI[name], pre, ws, dxr, status)
@@ -162,7 +162,7 @@ def test_linear_backward_parts():
     """Each gradient alone equals the one of the whole call."""
     d = Draw(9, BF)
     x, w, dout, pre = d.whole((200, 136)), d.whole((72, 136), 0.1), d.whole((200, 72)), d.whole((200, 72))
-    ws = torch.empty(M.moe_linear_backward_workspace_size(200, 136, 72, M.EPI_SILU, True), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(M.moe_linear_backward_workspace_size(200, 136, 72, M.EPI_SILU), dtype=torch.uint8, device="cuda")
     mk = lambda: [torch.zeros(s, dtype=BF, device="cuda") for s in ((200, 136), (72, 136), (72,))]  # noqa: E731
     whole = mk()
     M.moe_linear_backward(x, w, dout, *whole, M.EPI_SILU, pre, ws)
