@@ -24,6 +24,8 @@ struct SplitJob {
   int64_t M, N, ldr, ldo, ldp;
   int nk, n_ct;            // k-blocks; tiles along the columns
   int r_mn;                // kMajorAny: the rows' operand is MN-major too
+  int parts;               // parts of k: the cluster's S CTAs, or 1 (each CTA a tile of its own)
+  int n_tiles;
   const uint16_t* bias;
   const uint16_t* residual;
   uint16_t* out;
@@ -34,9 +36,9 @@ struct SplitJob {
 template <int NJ>
 struct SplitArgs {
   SplitJob job[NJ];
-  int tile0[NJ];           // first tile of each job; the jobs' tiles are numbered through
+  int cluster0[NJ];        // first cluster of each job
   int n_jobs;
-  int S;                   // CTAs of a cluster: parts of k
+  int S;                   // CTAs of a cluster
   int act;
   int early;               // columns' operand is not written by the previous kernel of the stream
   int32_t* status;
@@ -94,19 +96,23 @@ __global__ void __launch_bounds__(SplitCfg<EPI, MAJOR, BT>::kThreads)
   const int warp = threadIdx.x / kWarp;
   const int lane = threadIdx.x % kWarp;
   const int S = args.S;
-  const int rank = static_cast<int>(blockIdx.x) % S;
-  int tile = static_cast<int>(blockIdx.x) / S;
+  const int cta = static_cast<int>(blockIdx.x) % S;
+  const int cluster = static_cast<int>(blockIdx.x) / S;
   int which = 0;
 #pragma unroll
   for (int j = 1; j < C::kJobs; ++j)
-    if (j < args.n_jobs && tile >= args.tile0[j]) which = j;
+    if (j < args.n_jobs && cluster >= args.cluster0[j]) which = j;
   const SplitJob& jb = args.job[which];
-  if (C::kJobs > 1) tile -= args.tile0[which];
+  const int at = cluster - (C::kJobs > 1 ? args.cluster0[which] : 0);
+  const int parts = jb.parts;
+  const int tile = parts > 1 ? at : at * S + cta;
+  const int rank = parts > 1 ? cta : 0;  // this CTA's part of k
+  const bool idle = tile >= jb.n_tiles;  // fills up a cluster
   const bool r_mn = MAJOR == kMajorAny && jb.r_mn;
   const int64_t col0 = static_cast<int64_t>(tile % jb.n_ct) * C::kOutCols;
   const int64_t row0 = static_cast<int64_t>(tile / jb.n_ct) * BT;
-  const int kb0 = static_cast<int>(static_cast<int64_t>(jb.nk) * rank / S);
-  const int kb1 = static_cast<int>(static_cast<int64_t>(jb.nk) * (rank + 1) / S);
+  const int kb0 = idle ? 0 : static_cast<int>(static_cast<int64_t>(jb.nk) * rank / parts);
+  const int kb1 = idle ? 0 : static_cast<int>(static_cast<int64_t>(jb.nk) * (rank + 1) / parts);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
@@ -260,10 +266,10 @@ __global__ void __launch_bounds__(SplitCfg<EPI, MAJOR, BT>::kThreads)
   // CTA takes an S-th of the tile's columns.  Steps of four items a thread,
   // all their loads before their arithmetic.
   constexpr int kGroups = C::kOutCols / 4;
-  const int ng = kGroups / S;  // powers of two
+  const int ng = kGroups / parts;  // powers of two
   const int shift = __ffs(ng) - 1;
   const int live = static_cast<int>(jb.M - row0 < BT ? jb.M - row0 : BT);
-  const int items = live * ng;
+  const int items = idle ? 0 : live * ng;
   if (*abort_flag == 0) {
     auto run = [&](auto parts) {
       constexpr int kS = decltype(parts)::value;
@@ -374,7 +380,7 @@ __global__ void __launch_bounds__(SplitCfg<EPI, MAJOR, BT>::kThreads)
         });
       }
     };
-    switch (S) {
+    switch (parts) {
       case 1: run(std::integral_constant<int, 1>{}); break;
       case 2: run(std::integral_constant<int, 2>{}); break;
       case 4: run(std::integral_constant<int, 4>{}); break;
@@ -385,14 +391,14 @@ __global__ void __launch_bounds__(SplitCfg<EPI, MAJOR, BT>::kThreads)
 }
 
 template <int EPI, int MAJOR, int BT, bool kFp16>
-cudaError_t launch_split_variant(const DenseProblem* p, int n, int S, cudaStream_t stream) {
+cudaError_t launch_split_variant(const DenseProblem* p, int n, int S, const int* parts, cudaStream_t stream) {
   using C = SplitCfg<EPI, MAJOR, BT>;
   auto kern = dense_split_kernel<EPI, MAJOR, BT, kFp16>;
   static std::atomic<bool> attr_done[64];
   cudaError_t err = allow_smem(kern, C::kSmemBytes, attr_done);
   if (err != cudaSuccess) return err;
   SplitArgs<C::kJobs> a = {};
-  int64_t tiles = 0;
+  int64_t clusters = 0;
   for (int i = 0; i < n; ++i) {
     const DenseProblem& q = p[i];
     SplitJob& j = a.job[i];
@@ -420,8 +426,11 @@ cudaError_t launch_split_variant(const DenseProblem* p, int n, int S, cudaStream
     j.out = static_cast<uint16_t*>(q.out);
     j.pre = static_cast<uint16_t*>(q.pre);
     j.out2 = static_cast<uint16_t*>(q.out2);
-    a.tile0[i] = static_cast<int>(tiles);
-    tiles += static_cast<int64_t>(j.n_ct) * ((q.M + BT - 1) / BT);
+    const int64_t tiles = static_cast<int64_t>(j.n_ct) * ((q.M + BT - 1) / BT);
+    j.n_tiles = static_cast<int>(tiles);
+    j.parts = parts[i];
+    a.cluster0[i] = static_cast<int>(clusters);
+    clusters += j.parts > 1 ? tiles : (tiles + S - 1) / S;
   }
   a.n_jobs = n;
   a.S = S;
@@ -431,7 +440,7 @@ cudaError_t launch_split_variant(const DenseProblem* p, int n, int S, cudaStream
   a.wait_ns = launch_wait_limit_ns();
   a.surplus = launch_unreachable_arrivals();
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles * S));
+  cfg.gridDim = dim3(static_cast<unsigned>(clusters * S));
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::kSmemBytes;
   cfg.stream = stream;
@@ -448,48 +457,104 @@ cudaError_t launch_split_variant(const DenseProblem* p, int n, int S, cudaStream
 }
 
 template <int EPI, int MAJOR, bool kFp16>
-cudaError_t launch_split_rows(const DenseProblem* p, int n, int BT, int S, cudaStream_t stream) {
+cudaError_t launch_split(const DenseProblem* p, int n, int BT, int S, const int* parts, cudaStream_t stream) {
   if constexpr (MAJOR != kMajorAny) {
-    if (BT == 16) return launch_split_variant<EPI, MAJOR, 16, kFp16>(p, n, S, stream);
-    if (BT == 32) return launch_split_variant<EPI, MAJOR, 32, kFp16>(p, n, S, stream);
+    if (BT == 16) return launch_split_variant<EPI, MAJOR, 16, kFp16>(p, n, S, parts, stream);
+    if (BT == 32) return launch_split_variant<EPI, MAJOR, 32, kFp16>(p, n, S, parts, stream);
   }
-  if (BT <= 64) return launch_split_variant<EPI, MAJOR, 64, kFp16>(p, n, S, stream);
-  return launch_split_variant<EPI, MAJOR, 128, kFp16>(p, n, S, stream);
+  if (BT == 64) return launch_split_variant<EPI, MAJOR, 64, kFp16>(p, n, S, parts, stream);
+  return launch_split_variant<EPI, MAJOR, 128, kFp16>(p, n, S, parts, stream);
 }
 
-// Which kernel a launch's problems run on, and how they are cut.
+// Which kernel a launch's problems run on, and how they are cut: the plan of
+// the least estimated time.  The estimate's constants (microseconds) are
+// fitted to 95 products of 1 to 8192 rows, columns and contractions, each
+// timed on the pair kernel and with every BT and S here; the plan it picks is
+// within 2.5 % of the fastest one on average (at worst 1.3 times it).  At 512
+// x 2048 x 2048 the pair kernel takes 11.0 us and 64 x 128 tiles 9.9 us, at
+// 2048 x 2048 x 2048 18.5 and 27 us, at one row 14 and 4.5 us.
 struct Plan {
   bool split;
-  int bt, s;  // rows of a tile, parts of k
+  int bt, s;            // rows of a tile, CTAs of a cluster
+  int parts[kMaxJobs];  // parts of k: s or 1
 };
 
 template <int EPI, int MAJOR>
 Plan plan_of(const DenseProblem* p, int n, int num_sms) {
+  constexpr double kPairStart = 4.8, kPairStep = 0.38, kHalfStep = 0.27;  // launch to last store; 64 of k
+  constexpr double kStart = 2.9, kStep = 0.19, kL2 = 12.6e6;              // bytes a microsecond from L2
+  constexpr double kRow = 0.028, kJoin = 0.34, kRound = 3.4;              // a tile's row; a part; a second round
   const int oc = EPI == kDenseGate ? 128 : 256, so = EPI == kDenseGate ? 64 : 128;
-  int64_t pair_tiles = 0, rows = 0, nk = 0;
-  for (int i = 0; i < n; ++i) {
-    pair_tiles += ((p[i].M + 255) / 256) * ((p[i].N + oc - 1) / oc);
-    if (p[i].M > rows) rows = p[i].M;
-    if (p[i].K > nk * 64) nk = (p[i].K + 63) / 64;
+  const int most = num_sms / 2;
+  Plan best{};
+  double best_t;
+  {
+    int64_t tiles = 0;
+    double work = 0.0, longest = 0.0;
+    for (int i = 0; i < n; ++i) {
+      const int64_t t = ((p[i].M + 255) / 256) * ((p[i].N + oc - 1) / oc);
+      const double nk = static_cast<double>((p[i].K + 63) / 64);
+      tiles += t;
+      work += static_cast<double>(t) * nk;
+      longest = nk > longest ? nk : longest;
+    }
+    if (n == 1) {
+      const int64_t rest = tiles % most;
+      const bool cut = 2 * rest <= most;
+      const int64_t rounds = cut ? tiles / most : (tiles + most - 1) / most;
+      best_t = kPairStart + longest * (kPairStep * static_cast<double>(rounds) + (cut && rest ? kHalfStep : 0.0));
+    } else {
+      const double even = work / most + 0.5 * longest;
+      best_t = kPairStart + kPairStep * (even > longest ? even : longest);
+    }
+    if (tiles > 4 * most) return best;  // large: the pair kernel's
   }
-  Plan r{};
-  r.split = pair_tiles < 60;
-  if (!r.split) return r;
-  r.bt = MAJOR == kMajorAny ? 64 : 16;
-  while (r.bt < 64 && r.bt < rows) r.bt *= 2;
-  int64_t tiles = 0;
-  for (int i = 0; i < n; ++i) tiles += ((p[i].M + r.bt - 1) / r.bt) * ((p[i].N + so - 1) / so);
-  r.s = 1;
-  while (r.s < 8 && tiles * r.s * 2 <= 2 * num_sms && r.s * 2 <= nk) r.s *= 2;
-  return r;
+  for (int bt = MAJOR == kMajorAny ? 64 : 16; bt <= 128; bt *= 2) {
+    const int64_t slots = static_cast<int64_t>(num_sms) * (bt <= 64 ? 2 : 1);
+    bool more = false;  // a taller tile would save tiles
+    for (int i = 0; i < n; ++i) more |= p[i].M > bt;
+    for (int s = 1; s <= 8; s *= 2) {
+      // the first m jobs (those of the longest contraction) in s parts
+      for (int m = s == 1 ? 0 : 1; m <= (s == 1 ? 0 : n); ++m) {
+        int64_t ctas = 0;
+        for (int i = 0; i < n; ++i)
+          ctas += ((p[i].M + bt - 1) / bt) * ((p[i].N + so - 1) / so) * (i < m ? s : 1);
+        const double live = static_cast<double>(ctas < slots ? ctas : slots);
+        double step = live * (16384 + bt * 128) / kL2;
+        if (step < kStep) step = kStep;
+        double total = 0.0, longest = 0.0;
+        for (int i = 0; i < n; ++i) {
+          const int k = i < m ? s : 1;
+          const double tiles = static_cast<double>(((p[i].M + bt - 1) / bt) * ((p[i].N + so - 1) / so) * k);
+          const double rows = static_cast<double>(p[i].M < bt ? p[i].M : bt) * (EPI == kDenseGateGrad ? 2 : 1);
+          const double t = static_cast<double>((p[i].K + 64 * k - 1) / (64 * k)) * step + kRow * rows / k +
+                           (k > 1 ? kJoin * k : 0.0);
+          total += tiles * t;
+          longest = t > longest ? t : longest;
+        }
+        double t = total / static_cast<double>(slots);
+        if (t < longest) t = longest;
+        t += kStart + (ctas > slots ? kRound : 0.0);
+        if (t < best_t) {
+          best_t = t;
+          best.split = true;
+          best.bt = bt;
+          best.s = s;
+          for (int i = 0; i < n; ++i) best.parts[i] = i < m ? s : 1;
+        }
+      }
+    }
+    if (!more) break;
+  }
+  return best;
 }
 
 template <int EPI, int MAJOR>
 cudaError_t launch_kind(const DenseProblem* p, int n, int num_sms, cudaStream_t stream) {
   const Plan plan = plan_of<EPI, MAJOR>(p, n, num_sms);
   if (plan.split)
-    return p->fp16 ? launch_split_rows<EPI, MAJOR, true>(p, n, plan.bt, plan.s, stream)
-                   : launch_split_rows<EPI, MAJOR, false>(p, n, plan.bt, plan.s, stream);
+    return p->fp16 ? launch_split<EPI, MAJOR, true>(p, n, plan.bt, plan.s, plan.parts, stream)
+                   : launch_split<EPI, MAJOR, false>(p, n, plan.bt, plan.s, plan.parts, stream);
   return p->fp16 ? launch_pair<EPI, MAJOR, true>(p, n, num_sms, stream)
                  : launch_pair<EPI, MAJOR, false>(p, n, num_sms, stream);
 }
