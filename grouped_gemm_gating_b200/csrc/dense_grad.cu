@@ -33,7 +33,7 @@ __device__ __forceinline__ void unpack(uint4 v, float (&f)[8]) {
 }
 
 template <bool kFp16>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 3)
     dz_kernel(const uint16_t* dout, int64_t ldd, const uint16_t* pre, int64_t ldp, int64_t T, int64_t N, int act,
               uint16_t* dz, uint16_t* dbias) {
   __shared__ float sums[kThreads / kWarp][kCols];
@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(kThreads)
   const int64_t col = static_cast<int64_t>(blockIdx.x) * kCols + (lane & 7) * 8;
   const int64_t t0 = T * blockIdx.y / kParts, t1 = T * (blockIdx.y + 1) / kParts;
   float s[8] = {};
-  if (col < N) {
+  auto rows = [&](auto act_c) {
     for (int64_t t = t0 + threadIdx.x / 8; t < t1; t += kUnroll * kRows) {
       uint4 d4[kUnroll], z4[kUnroll];
 #pragma unroll
@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             float slope;
-            act_value_slope(z[i], act, &slope);
+            act_value_slope(z[i], decltype(act_c)::value, &slope);
             d[i] *= slope;
           }
 #pragma unroll
@@ -78,7 +78,8 @@ __global__ void __launch_bounds__(kThreads)
         for (int i = 0; i < 8; ++i) s[i] += d[i];
       }
     }
-  }
+  };
+  if (col < N) with_act(act, rows);
   if (dbias == nullptr) return;  // the same in every block of the cluster
 #pragma unroll
   for (int i = 0; i < 8; ++i) {

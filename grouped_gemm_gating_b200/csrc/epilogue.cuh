@@ -4,6 +4,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cstdint>
+#include <type_traits>
 
 #include "common.cuh"
 
@@ -84,6 +85,19 @@ __device__ __forceinline__ float act_value_slope(float z, int act, float* slope)
     default:
       *slope = 1.0f;
       return z;
+  }
+}
+
+// Runs f with the activation as a compile-time constant.
+template <class F>
+__device__ __forceinline__ void with_act(int act, F&& f) {
+  switch (act) {
+    case MOE_EPI_SILU: f(std::integral_constant<int, MOE_EPI_SILU>{}); break;
+    case MOE_EPI_GELU: f(std::integral_constant<int, MOE_EPI_GELU>{}); break;
+    case MOE_EPI_GELU_TANH: f(std::integral_constant<int, MOE_EPI_GELU_TANH>{}); break;
+    case MOE_EPI_RELU: f(std::integral_constant<int, MOE_EPI_RELU>{}); break;
+    case MOE_EPI_RELU2: f(std::integral_constant<int, MOE_EPI_RELU2>{}); break;
+    default: f(std::integral_constant<int, MOE_EPI_NONE>{}); break;
   }
 }
 
