@@ -40,7 +40,7 @@ __device__ __forceinline__ void unpack_vec(uint4 v, int dtype, float (&f)[8], in
   *n = 8;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 p = dtype == MOE_FP16 ? unpack2<true>(w[i]) : unpack2<false>(w[i]);
+    const float2 p = split(dtype == MOE_FP16 ? unpack2<true>(w[i]) : unpack2<false>(w[i]));
     f[2 * i] = p.x;
     f[2 * i + 1] = p.y;
   }
@@ -49,7 +49,7 @@ __device__ __forceinline__ void unpack_vec(uint4 v, int dtype, float (&f)[8], in
 __device__ __forceinline__ float load_one(const void* p, int64_t i, int dtype) {
   if (dtype == MOE_FP32) return static_cast<const float*>(p)[i];
   const uint16_t b = static_cast<const uint16_t*>(p)[i];
-  return dtype == MOE_FP16 ? unpack2<true>(b).x : unpack2<false>(b).x;
+  return split(dtype == MOE_FP16 ? unpack2<true>(b) : unpack2<false>(b)).x;
 }
 
 __device__ __forceinline__ void store_one(void* p, int64_t i, int dtype, float v) {

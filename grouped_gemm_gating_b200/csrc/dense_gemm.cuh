@@ -107,23 +107,6 @@ __device__ __forceinline__ void pin(uint32_t (&r)[COLS]) {  // uses stay after t
   for (int j = 0; j < COLS; ++j) asm volatile("" : "+r"(r[j]));
 }
 
-template <bool kFp16>
-__device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 p = unpack2<kFp16>(w[i]);
-    f[2 * i] = p.x;
-    f[2 * i + 1] = p.y;
-  }
-}
-
-template <bool kFp16>
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack2<kFp16>(f[0], f[1]), pack2<kFp16>(f[2], f[3]), pack2<kFp16>(f[4], f[5]),
-                    pack2<kFp16>(f[6], f[7]));
-}
-
 template <int EPI, int MAJOR, bool kFp16>
 __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
     dense_gemm_kernel(const __grid_constant__ Args<Cfg<EPI, MAJOR>::kJobs> args) {
@@ -509,25 +492,25 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
           with_act(MAJOR == kMajorKK ? args.act : MOE_EPI_NONE, [&](auto act) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              float v[8];
+              F2 v[4];
 #pragma unroll
-              for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(a[8 * i + j]);
+              for (int j = 0; j < 4; ++j) v[j] = f2_bits(a[8 * i + 2 * j], a[8 * i + 2 * j + 1]);
               if constexpr (MAJOR == kMajorKK) {
                 if (jb.bias != nullptr) {
-                  float bv[8];
+                  F2 bv[4];
                   unpack8<kFp16>(bias[i], bv);
 #pragma unroll
-                  for (int j = 0; j < 8; ++j) v[j] += bv[j];
+                  for (int j = 0; j < 4; ++j) v[j] = v[j] + bv[j];
                 }
                 if (jb.keep_pre) *cell(b + 1, i) = pack8<kFp16>(v);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = act_value(v[j], decltype(act)::value);
+                for (int j = 0; j < 4; ++j) v[j] = act_value<decltype(act)::value>(v[j]);
               }
               if (jb.residual) {
-                float r[8];
+                F2 r[4];
                 unpack8<kFp16>(*cell(b, i), r);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] += r[j];
+                for (int j = 0; j < 4; ++j) v[j] = v[j] + r[j];
               }
               *cell(b, i) = pack8<kFp16>(v);
             }
@@ -541,12 +524,12 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
           with_act(args.act, [&](auto act) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              float g[8], w[8], h[8];
+              F2 g[4], w[4], h[4];
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                g[j] = __uint_as_float(a[8 * i + j]);
-                w[j] = __uint_as_float(up[8 * i + j]);
-                h[j] = act_value(g[j], decltype(act)::value) * w[j];
+              for (int j = 0; j < 4; ++j) {
+                g[j] = f2_bits(a[8 * i + 2 * j], a[8 * i + 2 * j + 1]);
+                w[j] = f2_bits(up[8 * i + 2 * j], up[8 * i + 2 * j + 1]);
+                h[j] = act_value<decltype(act)::value>(g[j]) * w[j];
               }
               *cell(b, i) = pack8<kFp16>(h);
               if (gate_keep) {
@@ -561,14 +544,14 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
           with_act(args.act, [&](auto act) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              float g[8], up[8], h[8], dg[8], du[8];
+              F2 g[4], up[4], h[4], dg[4], du[4];
               unpack8<kFp16>(*cell(b, i), g);
               unpack8<kFp16>(*cell(b + 1, i), up);
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const float dh = __uint_as_float(a[8 * i + j]);
-                float slope;
-                const float v = act_value_slope(g[j], decltype(act)::value, &slope);
+              for (int j = 0; j < 4; ++j) {
+                const F2 dh = f2_bits(a[8 * i + 2 * j], a[8 * i + 2 * j + 1]);
+                F2 slope;
+                const F2 v = act_value_slope<decltype(act)::value>(g[j], &slope);
                 h[j] = v * up[j];
                 dg[j] = dh * up[j] * slope;
                 du[j] = dh * v;

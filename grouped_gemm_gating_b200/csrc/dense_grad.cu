@@ -19,18 +19,7 @@ constexpr int kCols = 64;
 constexpr int kThreads = 256;
 constexpr int kRows = kThreads / 8;  // rows of a block's step
 constexpr int kParts = 8;
-constexpr int kUnroll = 4;
-
-template <bool kFp16>
-__device__ __forceinline__ void unpack(uint4 v, float (&f)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 p = unpack2<kFp16>(w[i]);
-    f[2 * i] = p.x;
-    f[2 * i + 1] = p.y;
-  }
-}
+constexpr int kUnroll = 2;
 
 template <bool kFp16>
 __global__ void __launch_bounds__(kThreads, 3)
@@ -43,7 +32,7 @@ __global__ void __launch_bounds__(kThreads, 3)
   const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
   const int64_t col = static_cast<int64_t>(blockIdx.x) * kCols + (lane & 7) * 8;
   const int64_t t0 = T * blockIdx.y / kParts, t1 = T * (blockIdx.y + 1) / kParts;
-  float s[8] = {};
+  F2 s2[4] = {f2(0.0f), f2(0.0f), f2(0.0f), f2(0.0f)};
   auto rows = [&](auto act_c) {
     for (int64_t t = t0 + threadIdx.x / 8; t < t1; t += kUnroll * kRows) {
       uint4 d4[kUnroll], z4[kUnroll];
@@ -58,29 +47,33 @@ __global__ void __launch_bounds__(kThreads, 3)
       for (int k = 0; k < kUnroll; ++k) {
         const int64_t r = t + k * kRows;
         if (r >= t1) continue;
-        float d[8];
-        unpack<kFp16>(d4[k], d);
+        F2 d[4];
+        unpack8<kFp16>(d4[k], d);
         if (pre != nullptr) {
-          float z[8];
-          unpack<kFp16>(z4[k], z);
-          uint32_t o[4];
+          F2 z[4];
+          unpack8<kFp16>(z4[k], z);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            float slope;
-            act_value_slope(z[i], decltype(act_c)::value, &slope);
-            d[i] *= slope;
+          for (int i = 0; i < 4; ++i) {
+            F2 slope;
+            act_value_slope<decltype(act_c)::value>(z[i], &slope);
+            d[i] = d[i] * slope;
           }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o[i] = pack2<kFp16>(d[2 * i], d[2 * i + 1]);
-          *reinterpret_cast<uint4*>(dz + r * N + col) = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4*>(dz + r * N + col) = pack8<kFp16>(d);
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[i] += d[i];
+        for (int i = 0; i < 4; ++i) s2[i] = s2[i] + d[i];
       }
     }
   };
   if (col < N) with_act(act, rows);
   if (dbias == nullptr) return;  // the same in every block of the cluster
+  float s[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = split(s2[i]);
+    s[2 * i] = p.x;
+    s[2 * i + 1] = p.y;
+  }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     s[i] += __shfl_xor_sync(0xffffffffu, s[i], 8);

@@ -66,17 +66,14 @@ struct SplitCfg {
 };
 
 template <bool kFp16>
-__device__ __forceinline__ void unpack4(uint2 v, float (&f)[4]) {
-  const float2 a = unpack2<kFp16>(v.x), b = unpack2<kFp16>(v.y);
-  f[0] = a.x;
-  f[1] = a.y;
-  f[2] = b.x;
-  f[3] = b.y;
+__device__ __forceinline__ void unpack4(uint2 v, F2 (&f)[2]) {
+  f[0] = unpack2<kFp16>(v.x);
+  f[1] = unpack2<kFp16>(v.y);
 }
 
 template <bool kFp16>
-__device__ __forceinline__ void store4(uint16_t* p, const float (&f)[4]) {
-  *reinterpret_cast<uint2*>(p) = make_uint2(pack2<kFp16>(f[0], f[1]), pack2<kFp16>(f[2], f[3]));
+__device__ __forceinline__ void store4(uint16_t* p, const F2 (&f)[2]) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack2<kFp16>(f[0]), pack2<kFp16>(f[1]));
 }
 
 template <int EPI, int MAJOR, int BT, bool kFp16>
@@ -277,27 +274,23 @@ __global__ void __launch_bounds__(SplitCfg<EPI, MAJOR, BT>::kThreads)
       uint32_t base[kS];
 #pragma unroll
       for (int s = 0; s < kS; ++s) base[s] = kS == 1 ? part_addr : ptx::map_rank(part_addr, s);
-      auto sum_at = [&](int t, int c, float (&v)[4]) {
+      auto sum_at = [&](int t, int c, F2 (&v)[2]) {
         const uint32_t off = static_cast<uint32_t>(t * C::kPartStride + c) * 4;
         float4 p[kS];
 #pragma unroll
         for (int s = 0; s < kS; ++s)
           p[s] = kS == 1 ? *reinterpret_cast<const float4*>(part + t * C::kPartStride + c) : ptx::ld_cluster_f4(base[s] + off);
-        v[0] = p[0].x;
-        v[1] = p[0].y;
-        v[2] = p[0].z;
-        v[3] = p[0].w;
+        v[0] = f2(p[0].x, p[0].y);
+        v[1] = f2(p[0].z, p[0].w);
 #pragma unroll
         for (int s = 1; s < kS; ++s) {
-          v[0] += p[s].x;
-          v[1] += p[s].y;
-          v[2] += p[s].z;
-          v[3] += p[s].w;
+          v[0] = v[0] + f2(p[s].x, p[s].y);
+          v[1] = v[1] + f2(p[s].z, p[s].w);
         }
       };
       constexpr int kU = 4;
       for (int i0 = threadIdx.x; i0 < items; i0 += kU * C::kThreads) {
-        float v[kU][4], w[kU][4];
+        F2 v[kU][2], w[kU][2];
         uint2 x0[kU], x1[kU];  // residual or g; bias or u
         bool on[kU];
         int64_t rows[kU], cols[kU];
@@ -336,20 +329,20 @@ __global__ void __launch_bounds__(SplitCfg<EPI, MAJOR, BT>::kThreads)
             if constexpr (EPI == kDenseLinear) {
               if constexpr (MAJOR == kMajorKK) {
                 if (jb.bias != nullptr) {
-                  float b[4];
+                  F2 b[2];
                   unpack4<kFp16>(x1[k], b);
 #pragma unroll
-                  for (int j = 0; j < 4; ++j) v[k][j] += b[j];
+                  for (int j = 0; j < 2; ++j) v[k][j] = v[k][j] + b[j];
                 }
                 if (jb.pre != nullptr) store4<kFp16>(jb.pre + row * jb.ldp + col, v[k]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) v[k][j] = act_value(v[k][j], kAct);
+                for (int j = 0; j < 2; ++j) v[k][j] = act_value<kAct>(v[k][j]);
               }
               if (jb.residual != nullptr) {
-                float r[4];
+                F2 r[2];
                 unpack4<kFp16>(x0[k], r);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) v[k][j] += r[j];
+                for (int j = 0; j < 2; ++j) v[k][j] = v[k][j] + r[j];
               }
               store4<kFp16>(jb.out + row * jb.ldo + col, v[k]);
             } else if constexpr (EPI == kDenseGate) {
@@ -358,16 +351,16 @@ __global__ void __launch_bounds__(SplitCfg<EPI, MAJOR, BT>::kThreads)
                 store4<kFp16>(jb.pre + row * jb.ldp + jb.N + col, w[k]);
               }
 #pragma unroll
-              for (int j = 0; j < 4; ++j) v[k][j] = act_value(v[k][j], kAct) * w[k][j];
+              for (int j = 0; j < 2; ++j) v[k][j] = act_value<kAct>(v[k][j]) * w[k][j];
               store4<kFp16>(jb.out + row * jb.ldo + col, v[k]);
             } else {
-              float g[4], u[4], dg[4], du[4], h[4];
+              F2 g[2], u[2], dg[2], du[2], h[2];
               unpack4<kFp16>(x0[k], g);
               unpack4<kFp16>(x1[k], u);
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                float slope;
-                const float a = act_value_slope(g[j], kAct, &slope);
+              for (int j = 0; j < 2; ++j) {
+                F2 slope;
+                const F2 a = act_value_slope<kAct>(g[j], &slope);
                 h[j] = a * u[j];
                 dg[j] = v[k][j] * u[j] * slope;
                 du[j] = v[k][j] * a;
