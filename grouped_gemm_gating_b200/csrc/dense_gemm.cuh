@@ -225,6 +225,8 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
   // gate, with pre kept, has one set of three instead of several of one.
   const bool gate_keep = EPI == kDenseGate && args.job[0].keep_pre;
   const int n_sets = gate_keep ? 1 : 2;
+  auto set_of = [&](int chunk) { return gate_keep ? 0 : chunk & 1; };
+  auto phase_of = [&](int chunk) { return static_cast<uint32_t>((gate_keep ? chunk : chunk >> 1) & 1); };
   constexpr int kPerSet = C::kBufs / 2;
   auto fail = [&]() {
     *abort_flag = 1;
@@ -375,7 +377,7 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
           const Place p = place_of(t, group);
           if (c_f < p.chunks) {
             const Job& jb = args.job[t.job];
-            const int set = asked % n_sets;
+            const int set = set_of(asked);
             uint8_t* b = my_bufs + set * kPerSet * C::kBufBytes;
             const int col = p.col + c_f * 32;
             if (kFetch && EPI == kDenseGateGrad) {
@@ -403,8 +405,8 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
         const Job& jb = args.job[t.job];
         const Place p = place_of(t, group);
         for (int c = 0; c < p.chunks; ++c) {
-          const int set = stored % n_sets;
-          if (!ptx::mbar_wait_bounded(&my_written[set], (stored / n_sets) & 1, abort_flag, args.wait_ns)) {
+          const int set = set_of(stored);
+          if (!ptx::mbar_wait_bounded(&my_written[set], phase_of(stored), abort_flag, args.wait_ns)) {
             fail();
             ok = false;
             break;
@@ -431,7 +433,7 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
         }
       }
       // what was asked for lands, what was stored has left, before shared memory is given up
-      for (int i = stored; i < asked; ++i) ptx::mbar_wait_bounded(&my_ready[i % n_sets], (i / n_sets) & 1, never, kDrainLimitNs);
+      for (int i = stored; i < asked; ++i) ptx::mbar_wait_bounded(&my_ready[set_of(i)], phase_of(i), never, kDrainLimitNs);
       ptx::bulk_wait();
     }
   } else {
@@ -464,10 +466,10 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
 #pragma unroll 1
       for (int c = 0; c < p.chunks; ++c) {
         const int col = p.col + c * 32;
-        const int set = seq % n_sets;
+        const int set = set_of(seq);
         const int b = set * kPerSet;
         if (lane == 0)
-          bad = !ptx::mbar_wait_bounded(&ready[group * 2 + set], (seq / n_sets) & 1, abort_flag, args.wait_ns);
+          bad = !ptx::mbar_wait_bounded(&ready[group * 2 + set], phase_of(seq), abort_flag, args.wait_ns);
         if (__any_sync(0xffffffffu, bad)) {
           fail();
           ok = false;
@@ -570,7 +572,7 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
       if (!ok) break;
       ptx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive_leader(&tempty[abuf]);
+      if (lane == 0) ptx::mbar_arrive_leader_tmem(&tempty[abuf]);
       if (++abuf == 2) {
         abuf = 0;
         aphase ^= 1u;

@@ -313,6 +313,14 @@ __device__ __forceinline__ void mbar_arrive_leader(uint64_t* bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(leader_addr(bar)) : "memory");
 }
 
+// The same at block scope: for arrivals that hand over tensor memory alone
+// (ordered by the tcgen05 fences around them), not data in shared or global
+// memory.  A cluster-scope release first waits for all the thread's memory
+// operations; measured in an epilogue, 7000 to 9600 clocks a tile.
+__device__ __forceinline__ void mbar_arrive_leader_tmem(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(leader_addr(bar)) : "memory");
+}
+
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
