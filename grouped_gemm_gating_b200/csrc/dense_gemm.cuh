@@ -19,13 +19,15 @@
 // rows of the contraction; dW = dz^T x reads both so) are read MN-major.
 //
 // Two accumulators in tensor memory: the epilogue (two groups of four warps,
-// each on half of the columns) drains one while the MMA fills the other, 32
+// each on half of the columns) drains one while the MMA fills the other, 64
 // columns at a time.  Matrices move between shared and global memory by TMA
 // only, a warp of each group moving them: it fetches what the next chunks add
 // (a residual, or g and u) as soon as the buffers' last results have left,
-// and stores what the group has written in their place.  A thread per row
-// would touch 32 lines with every 16-byte access; measured at 8192 x 6144 x
-// 2048, dh with [dg | du] and h took 220 us that way.
+// and stores what the group has written in their place.  What bounds the
+// kernel is what an SM takes in (64 bytes a clock, and about 11 TB/s from L2
+// for all): a 64-wide K step brings 32 KB for 512 clocks of products, so the
+// epilogue's transfers are whole 128-byte lines (8192 x 6144 x 2048, dh with
+// [dg | du] and h: a thread per row 220 us, 64-byte rows by TMA 195 us).
 //
 // Tiles go in groups of kGroupM row tiles, column by column, so the pairs at
 // work share operand rows in L2.  The tiles that do not fill a last round of
@@ -84,8 +86,10 @@ struct Cfg {
   static constexpr int kABytes = 128 * 128;                          // 128 M values x 64 K
   static constexpr int kBBytes = BN / 2 * 128;                       // this CTA's half of B
   static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int kBufs = EPI == kDenseGateGrad ? 6 : 4;        // buffers of an epilogue group
-  static constexpr int kBufBytes = 128 * 64;                         // 128 rows x 32 columns
+  static constexpr int kSets = EPI == kDenseGateGrad ? 1 : 2;        // sets of buffers of an epilogue group
+  static constexpr int kPerSet = EPI == kDenseGateGrad ? 3 : 1;
+  static constexpr int kBufs = kSets * kPerSet;
+  static constexpr int kBufBytes = 128 * 128;                        // 128 rows x 64 columns
   static constexpr int kStages = EPI == kDenseGateGrad ? 4 : 5;
   static constexpr int kTmemCols = 2 * BN;
   static constexpr int kNumThreads = 384;  // producer, MMA, eight epilogue warps, two that move their data
@@ -205,29 +209,31 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
     const int v = i * n_pairs + (n_pairs - 1 - pair);
     return i * n_pairs == last && v < units ? v : -1;
   };
-  // Where an epilogue group's share of a unit lies: `chunks` times 32 columns
-  // from `col` of the output, from `acc` of the accumulator.
+  // Where an epilogue group's share of a unit lies: `chunks` times 64 columns
+  // from `col` of the output, from `acc` of the accumulator.  (Half a gate
+  // tile has 64 columns: the first group's.)
   struct Place {
     int m0, col, acc, chunks;
   };
   auto place_of = [&](const Unit& t, int group) {
     Place p;
     const bool whole = t.part < 0;
-    const int cols = C::kOutCols / (whole ? 2 : 4);
+    const int cols = EPI == kDenseGate ? 64 : whole ? 128 : 64;
     p.m0 = t.mt * 256 + rank * 128;
     p.acc = group * cols;
     p.col = t.nt * C::kOutCols + (t.part > 0 ? C::kOutCols / 2 : 0) + p.acc;
     const int64_t left = p.m0 < args.job[t.job].M ? args.job[t.job].N - p.col : 0;
-    p.chunks = left <= 0 ? 0 : left >= cols ? cols / 32 : static_cast<int>((left + 31) / 32);
+    p.chunks = left <= 0 ? 0 : left >= cols ? cols / 64 : static_cast<int>((left + 63) / 64);
+    if (EPI == kDenseGate && !whole && group == 1) p.chunks = 0;
     return p;
   };
-  // Sets of buffers: the output's (linear: and pre's; gate-grad: dg, du, h);
-  // gate, with pre kept, has one set of three instead of several of one.
-  const bool gate_keep = EPI == kDenseGate && args.job[0].keep_pre;
-  const int n_sets = gate_keep ? 1 : 2;
-  auto set_of = [&](int chunk) { return gate_keep ? 0 : chunk & 1; };
-  auto phase_of = [&](int chunk) { return static_cast<uint32_t>((gate_keep ? chunk : chunk >> 1) & 1); };
-  constexpr int kPerSet = C::kBufs / 2;
+  // A chunk is made in passes, one buffer each: pre first when it is kept
+  // (gate: g, then u), the output last.  Gate-grad: one pass, three buffers.
+  auto passes_of = [&](const Job& jb) {
+    return EPI == kDenseGateGrad || !jb.keep_pre ? 1 : EPI == kDenseGate ? 3 : 2;
+  };
+  auto set_of = [&](int pass) { return C::kSets == 1 ? 0 : pass & 1; };
+  auto phase_of = [&](int pass) { return static_cast<uint32_t>((C::kSets == 1 ? pass : pass >> 1) & 1); };
   auto fail = [&]() {
     *abort_flag = 1;
     set_status(args.status, MOE_ERR_DEVICE_TIMEOUT);
@@ -368,9 +374,8 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
       uint8_t* my_bufs = bufs + group * C::kBufs * C::kBufBytes;
       uint64_t* my_ready = ready + group * 2;
       uint64_t* my_written = written + group * 2;
-      constexpr bool kFetch = EPI == kDenseLinear || EPI == kDenseGateGrad;
-      int it_f = 0, c_f = 0, u_f = unit_at(0);  // next chunk to make ready
-      int asked = 0, stored = 0;                // chunks made ready, chunks stored
+      int it_f = 0, c_f = 0, s_f = 0, u_f = unit_at(0);  // next pass to make ready
+      int asked = 0, stored = 0;                         // passes made ready, passes stored
       auto make_ready = [&]() {
         while (u_f >= 0) {
           const Unit t = unit_of(u_f);
@@ -378,58 +383,65 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
           if (c_f < p.chunks) {
             const Job& jb = args.job[t.job];
             const int set = set_of(asked);
-            uint8_t* b = my_bufs + set * kPerSet * C::kBufBytes;
-            const int col = p.col + c_f * 32;
-            if (kFetch && EPI == kDenseGateGrad) {
+            uint8_t* b = my_bufs + set * C::kPerSet * C::kBufBytes;
+            const int col = p.col + c_f * 64;
+            const bool last_pass = s_f + 1 == passes_of(jb);
+            if constexpr (EPI == kDenseGateGrad) {
               ptx::mbar_arrive_expect_tx(&my_ready[set], 2 * C::kBufBytes);
               ptx::tma_load_3d(b, &jb.tm_res, &my_ready[set], col, 0, p.m0);
               ptx::tma_load_3d(b + C::kBufBytes, &jb.tm_res, &my_ready[set], col, 1, p.m0);
-            } else if (kFetch && jb.residual) {
+            } else if (EPI == kDenseLinear && jb.residual && last_pass) {
               ptx::mbar_arrive_expect_tx(&my_ready[set], C::kBufBytes);
               ptx::tma_load_2d(b, &jb.tm_res, &my_ready[set], col, p.m0);
             } else {
               ptx::mbar_arrive(&my_ready[set]);
             }
             ++asked;
-            ++c_f;
+            if (last_pass) {
+              s_f = 0;
+              ++c_f;
+            } else {
+              ++s_f;
+            }
             return;
           }
           c_f = 0;
           u_f = unit_at(++it_f);
         }
       };
-      for (int i = 0; i < n_sets; ++i) make_ready();
+      for (int i = 0; i < C::kSets; ++i) make_ready();
       bool ok = true;
       for (int it = 0, u; ok && (u = unit_at(it)) >= 0; ++it) {
         const Unit t = unit_of(u);
         const Job& jb = args.job[t.job];
         const Place p = place_of(t, group);
-        for (int c = 0; c < p.chunks; ++c) {
-          const int set = set_of(stored);
-          if (!ptx::mbar_wait_bounded(&my_written[set], phase_of(stored), abort_flag, args.wait_ns)) {
-            fail();
-            ok = false;
-            break;
-          }
-          const uint8_t* b = my_bufs + set * kPerSet * C::kBufBytes;
-          const int col = p.col + c * 32;
-          if constexpr (EPI == kDenseGateGrad) {
-            ptx::tma_store_3d(&jb.tm_out, b, col, 0, p.m0);
-            ptx::tma_store_3d(&jb.tm_out, b + C::kBufBytes, col, 1, p.m0);
-            ptx::tma_store_2d(&jb.tm_pre, b + 2 * C::kBufBytes, col, p.m0);
-          } else {
-            ptx::tma_store_2d(&jb.tm_out, b, col, p.m0);
-            if (EPI == kDenseGate && jb.keep_pre) {
-              ptx::tma_store_3d(&jb.tm_pre, b + C::kBufBytes, col, 0, p.m0);
-              ptx::tma_store_3d(&jb.tm_pre, b + 2 * C::kBufBytes, col, 1, p.m0);
-            } else if (jb.keep_pre) {
-              ptx::tma_store_2d(&jb.tm_pre, b + C::kBufBytes, col, p.m0);
+        const int passes = passes_of(jb);
+        for (int c = 0; ok && c < p.chunks; ++c) {
+          const int col = p.col + c * 64;
+          for (int s = 0; s < passes; ++s) {
+            const int set = set_of(stored);
+            if (!ptx::mbar_wait_bounded(&my_written[set], phase_of(stored), abort_flag, args.wait_ns)) {
+              fail();
+              ok = false;
+              break;
             }
+            const uint8_t* b = my_bufs + set * C::kPerSet * C::kBufBytes;
+            if constexpr (EPI == kDenseGateGrad) {
+              ptx::tma_store_3d(&jb.tm_out, b, col, 0, p.m0);
+              ptx::tma_store_3d(&jb.tm_out, b + C::kBufBytes, col, 1, p.m0);
+              ptx::tma_store_2d(&jb.tm_pre, b + 2 * C::kBufBytes, col, p.m0);
+            } else if (s + 1 == passes) {
+              ptx::tma_store_2d(&jb.tm_out, b, col, p.m0);
+            } else if (EPI == kDenseGate) {
+              ptx::tma_store_3d(&jb.tm_pre, b, col, s, p.m0);
+            } else {
+              ptx::tma_store_2d(&jb.tm_pre, b, col, p.m0);
+            }
+            ptx::bulk_commit();
+            ++stored;
+            ptx::bulk_wait_read();
+            make_ready();
           }
-          ptx::bulk_commit();
-          ++stored;
-          ptx::bulk_wait_read();
-          make_ready();
         }
       }
       // what was asked for lands, what was stored has left, before shared memory is given up
@@ -444,11 +456,11 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
     uint8_t* my_bufs = bufs + group * C::kBufs * C::kBufBytes;
     // 16-byte cell j (8 columns) of this thread's row in buffer b
     auto cell = [&](int b, int j) {
-      return reinterpret_cast<uint4*>(my_bufs + b * C::kBufBytes + r128 * 64 + ((j ^ ((r128 >> 1) & 3)) << 4));
+      return reinterpret_cast<uint4*>(my_bufs + b * C::kBufBytes + r128 * 128 + ((j ^ (r128 & 7)) << 4));
     };
     int abuf = 0;
     uint32_t aphase = 0;
-    int seq = 0;  // chunks done
+    int seq = 0;  // passes done
     bool ok = true;
     for (int it = 0, u; ok && (u = unit_at(it)) >= 0; ++it) {
       const Unit t = unit_of(u);
@@ -463,11 +475,15 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
       ptx::tc_fence_after();
       const uint32_t t_acc =
           tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(abuf * BN + p.acc);
+      const int passes = passes_of(jb);
+      const int n_steps = p.chunks * passes;
 #pragma unroll 1
-      for (int c = 0; c < p.chunks; ++c) {
-        const int col = p.col + c * 32;
+      for (int i2 = 0; i2 < n_steps; ++i2) {
+        const int c = passes == 1 ? i2 : passes == 2 ? i2 >> 1 : i2 / 3;
+        const int pass = i2 - c * passes;
+        const bool last_pass = pass + 1 == passes;
         const int set = set_of(seq);
-        const int b = set * kPerSet;
+        const int b = set * C::kPerSet;
         if (lane == 0)
           bad = !ptx::mbar_wait_bounded(&ready[group * 2 + set], phase_of(seq), abort_flag, args.wait_ns);
         if (__any_sync(0xffffffffu, bad)) {
@@ -475,94 +491,108 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
           ok = false;
           break;
         }
-        uint32_t a[32];
-        if (EPI != kDenseLinear || jb.nk > 0) {
-          tmem_ld(t_acc + c * 32, a);
-        } else {
+#pragma unroll 1
+        for (int s = 0; s < 2; ++s) {
+          const int col = p.col + c * 64 + s * 32;
+          const uint32_t at = t_acc + c * 64 + s * 32;
+          uint32_t a[32];
+          if constexpr (EPI == kDenseLinear) {
+            uint4 bias[4];
+            if (MAJOR == kMajorKK && jb.bias != nullptr) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) a[j] = 0u;
-        }
-        if constexpr (EPI == kDenseLinear) {
-          uint4 bias[4];
-          if (MAJOR == kMajorKK && jb.bias != nullptr) {
+              for (int i = 0; i < 4; ++i)
+                if (col + 8 * i < jb.N) bias[i] = *reinterpret_cast<const uint4*>(jb.bias + col + 8 * i);
+            }
+            if (jb.nk > 0) {
+              tmem_ld(at, a);
+              ptx::tmem_wait_ld();
+              pin(a);
+            } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (col + 8 * i < jb.N) bias[i] = *reinterpret_cast<const uint4*>(jb.bias + col + 8 * i);
-          }
-          ptx::tmem_wait_ld();
-          pin(a);
-          with_act(MAJOR == kMajorKK ? args.act : MOE_EPI_NONE, [&](auto act) {
+              for (int j = 0; j < 32; ++j) a[j] = 0u;
+            }
+            with_act(MAJOR == kMajorKK && last_pass ? args.act : MOE_EPI_NONE, [&](auto act) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              F2 v[4];
+              for (int i = 0; i < 4; ++i) {
+                F2 v[4];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) v[j] = f2_bits(a[8 * i + 2 * j], a[8 * i + 2 * j + 1]);
-              if constexpr (MAJOR == kMajorKK) {
-                if (jb.bias != nullptr) {
-                  F2 bv[4];
-                  unpack8<kFp16>(bias[i], bv);
+                for (int j = 0; j < 4; ++j) v[j] = f2_bits(a[8 * i + 2 * j], a[8 * i + 2 * j + 1]);
+                if constexpr (MAJOR == kMajorKK) {
+                  if (jb.bias != nullptr) {
+                    F2 bv[4];
+                    unpack8<kFp16>(bias[i], bv);
 #pragma unroll
-                  for (int j = 0; j < 4; ++j) v[j] = v[j] + bv[j];
+                    for (int j = 0; j < 4; ++j) v[j] = v[j] + bv[j];
+                  }
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) v[j] = act_value<decltype(act)::value>(v[j]);
                 }
-                if (jb.keep_pre) *cell(b + 1, i) = pack8<kFp16>(v);
+                if (jb.residual && last_pass) {
+                  F2 r[4];
+                  unpack8<kFp16>(*cell(b, s * 4 + i), r);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] = act_value<decltype(act)::value>(v[j]);
+                  for (int j = 0; j < 4; ++j) v[j] = v[j] + r[j];
+                }
+                *cell(b, s * 4 + i) = pack8<kFp16>(v);
               }
-              if (jb.residual) {
-                F2 r[4];
-                unpack8<kFp16>(*cell(b, i), r);
+            });
+          } else if constexpr (EPI == kDenseGate) {
+            const uint32_t u_at = at + (t.part < 0 ? BN / 2 : BN / 4);
+            if (!last_pass) {  // g or u as it is
+              tmem_ld(pass == 0 ? at : u_at, a);
+              ptx::tmem_wait_ld();
+              pin(a);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] = v[j] + r[j];
+              for (int i = 0; i < 4; ++i) {
+                F2 v[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] = f2_bits(a[8 * i + 2 * j], a[8 * i + 2 * j + 1]);
+                *cell(b, s * 4 + i) = pack8<kFp16>(v);
               }
-              *cell(b, i) = pack8<kFp16>(v);
+            } else {
+              uint32_t up[32];
+              tmem_ld(at, a);
+              tmem_ld(u_at, up);
+              ptx::tmem_wait_ld();
+              pin(a);
+              pin(up);
+              with_act(args.act, [&](auto act) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  F2 h[4];
+#pragma unroll
+                  for (int j = 0; j < 4; ++j)
+                    h[j] = act_value<decltype(act)::value>(f2_bits(a[8 * i + 2 * j], a[8 * i + 2 * j + 1])) *
+                           f2_bits(up[8 * i + 2 * j], up[8 * i + 2 * j + 1]);
+                  *cell(b, s * 4 + i) = pack8<kFp16>(h);
+                }
+              });
             }
-          });
-        } else if constexpr (EPI == kDenseGate) {
-          uint32_t up[32];
-          tmem_ld(t_acc + (t.part < 0 ? BN / 2 : BN / 4) + c * 32, up);
-          ptx::tmem_wait_ld();
-          pin(a);
-          pin(up);
-          with_act(args.act, [&](auto act) {
+          } else {
+            tmem_ld(at, a);
+            ptx::tmem_wait_ld();
+            pin(a);
+            with_act(args.act, [&](auto act) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              F2 g[4], w[4], h[4];
+              for (int i = 0; i < 4; ++i) {
+                F2 g[4], up[4], h[4], dg[4], du[4];
+                unpack8<kFp16>(*cell(b, s * 4 + i), g);
+                unpack8<kFp16>(*cell(b + 1, s * 4 + i), up);
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                g[j] = f2_bits(a[8 * i + 2 * j], a[8 * i + 2 * j + 1]);
-                w[j] = f2_bits(up[8 * i + 2 * j], up[8 * i + 2 * j + 1]);
-                h[j] = act_value<decltype(act)::value>(g[j]) * w[j];
+                for (int j = 0; j < 4; ++j) {
+                  const F2 dh = f2_bits(a[8 * i + 2 * j], a[8 * i + 2 * j + 1]);
+                  F2 slope;
+                  const F2 v = act_value_slope<decltype(act)::value>(g[j], &slope);
+                  h[j] = v * up[j];
+                  dg[j] = dh * up[j] * slope;
+                  du[j] = dh * v;
+                }
+                *cell(b, s * 4 + i) = pack8<kFp16>(dg);
+                *cell(b + 1, s * 4 + i) = pack8<kFp16>(du);
+                *cell(b + 2, s * 4 + i) = pack8<kFp16>(h);
               }
-              *cell(b, i) = pack8<kFp16>(h);
-              if (gate_keep) {
-                *cell(b + 1, i) = pack8<kFp16>(g);
-                *cell(b + 2, i) = pack8<kFp16>(w);
-              }
-            }
-          });
-        } else {
-          ptx::tmem_wait_ld();
-          pin(a);
-          with_act(args.act, [&](auto act) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              F2 g[4], up[4], h[4], dg[4], du[4];
-              unpack8<kFp16>(*cell(b, i), g);
-              unpack8<kFp16>(*cell(b + 1, i), up);
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const F2 dh = f2_bits(a[8 * i + 2 * j], a[8 * i + 2 * j + 1]);
-                F2 slope;
-                const F2 v = act_value_slope<decltype(act)::value>(g[j], &slope);
-                h[j] = v * up[j];
-                dg[j] = dh * up[j] * slope;
-                du[j] = dh * v;
-              }
-              *cell(b, i) = pack8<kFp16>(dg);
-              *cell(b + 1, i) = pack8<kFp16>(du);
-              *cell(b + 2, i) = pack8<kFp16>(h);
-            }
-          });
+            });
+          }
         }
         ptx::fence_proxy_async_smem();
         __syncwarp();
@@ -616,7 +646,7 @@ inline bool encode_rows(CUtensorMap* m, bool fp16, const void* p, uint64_t rows,
 inline bool encode_halves(CUtensorMap* m, bool fp16, const void* p, uint64_t rows, uint64_t cols, uint64_t ld,
                           uint32_t box_rows) {
   const uint64_t dims[3] = {cols, 2, rows}, st[2] = {cols * 2, ld * 2};
-  const uint32_t box[3] = {32, 1, box_rows};
+  const uint32_t box[3] = {64, 1, box_rows};
   return encode_16bit(m, fp16, p, 3, dims, st, box);
 }
 
@@ -648,17 +678,17 @@ bool make_job(const DenseProblem& p, Job* a) {
   }
   if (EPI == kDenseGateGrad) {
     ok = ok && encode_halves(&a->tm_out, kFp16, p.out, M, N, p.ldo, 128) &&
-         encode_rows(&a->tm_pre, kFp16, p.out2, M, N, N, 32, 128) &&
+         encode_rows(&a->tm_pre, kFp16, p.out2, M, N, N, 64, 128) &&
          encode_halves(&a->tm_res, kFp16, p.pre, M, N, p.ldp, 128);
   } else {
-    ok = ok && encode_rows(&a->tm_out, kFp16, p.out, M, N, p.ldo, 32, 128);
+    ok = ok && encode_rows(&a->tm_out, kFp16, p.out, M, N, p.ldo, 64, 128);
     a->keep_pre = p.pre != nullptr;
     if (p.pre != nullptr)
       ok = ok && (EPI == kDenseGate ? encode_halves(&a->tm_pre, kFp16, p.pre, M, N, p.ldp, 128)
-                                    : encode_rows(&a->tm_pre, kFp16, p.pre, M, N, p.ldp, 32, 128));
+                                    : encode_rows(&a->tm_pre, kFp16, p.pre, M, N, p.ldp, 64, 128));
   }
   a->residual = p.residual != nullptr;
-  if (a->residual) ok = ok && encode_rows(&a->tm_res, kFp16, p.residual, M, N, p.ldr, 32, 128);
+  if (a->residual) ok = ok && encode_rows(&a->tm_res, kFp16, p.residual, M, N, p.ldr, 64, 128);
   a->M = p.M;
   a->N = p.N;
   a->a_mn = a_mn;

@@ -29,9 +29,8 @@ moe_status finish(cudaError_t err, int launches);
 
 int num_sms_current_device();
 
-// Tiled tensor map of 16-bit elements, zero fill out of bounds; dims and box
-// innermost first, strides in bytes for dims 1..  The box's rows are 128 or
-// 64 bytes, and so is the swizzle.
+// Tiled tensor map of 16-bit elements, 128-byte swizzle, zero fill out of
+// bounds; dims and box innermost first, strides in bytes for dims 1..
 bool encode_16bit(CUtensorMap* map, bool fp16, const void* base, int rank, const uint64_t* dims,
                   const uint64_t* strides, const uint32_t* box);
 
