@@ -460,12 +460,13 @@ cudaError_t launch_split(const DenseProblem* p, int n, int BT, int S, const int*
 }
 
 // Which kernel a launch's problems run on, and how they are cut: the plan of
-// the least estimated time.  The estimate's constants (microseconds) are
-// fitted to 95 products of 1 to 8192 rows, columns and contractions, each
-// timed on the pair kernel and with every BT and S here; the plan it picks is
-// within 2.5 % of the fastest one on average (at worst 1.3 times it).  At 512
-// x 2048 x 2048 the pair kernel takes 11.0 us and 64 x 128 tiles 9.9 us, at
-// 2048 x 2048 x 2048 18.5 and 27 us, at one row 14 and 4.5 us.
+// the least estimated time.  The estimate's constants (microseconds, bytes a
+// microsecond) are fitted to 150 products of 1 to 8192 rows, columns and
+// contractions, each timed on the pair kernel and with every BT and S here;
+// the plan it picks is within 1.5 % of the fastest one on average, and at
+// worst 1.4 times it.  At one row of 2048 x 2048 the pair kernel takes 14 us
+// and 16 x 128 tiles in 8 parts 4.3 us; at 512 rows 11.5 and (64 x 128, whole)
+// 9.9 us; at 2048 rows 19.5 and 27 us.
 struct Plan {
   bool split;
   int bt, s;            // rows of a tile, CTAs of a cluster
@@ -474,33 +475,43 @@ struct Plan {
 
 template <int EPI, int MAJOR>
 Plan plan_of(const DenseProblem* p, int n, int num_sms) {
-  constexpr double kPairStart = 4.8, kPairStep = 0.38, kHalfStep = 0.27;  // launch to last store; 64 of k
-  constexpr double kStart = 2.9, kStep = 0.19, kL2 = 12.6e6;              // bytes a microsecond from L2
-  constexpr double kRow = 0.028, kJoin = 0.34, kRound = 3.4;              // a tile's row; a part; a second round
+  // pair kernel: launch to last store, 64 of k of a tile and of half a tile, whole tiles' longer end
+  constexpr double kPairStart = 5.5 + (EPI == kDenseGateGrad ? 1.9 : 0.0), kPairStep = 0.39, kHalfStep = 0.255;
+  constexpr double kPairEnd = 1.1, kPairHbm = 3.65e6;
+  // here: launch to last store, 64 of k, stages' bytes of all SMs, a row's and a part's epilogue, 128-row tiles
+  // (one CTA an SM), a second round of CTAs
+  constexpr double kStart = 4.07, kStep = 0.154, kFill = 12.2e6, kHbm = 8.6e6;
+  constexpr double kRow = 0.0081, kJoin = 0.154, kTall = 1.26, kRound = 3.2;
   const int oc = EPI == kDenseGate ? 128 : 256, so = EPI == kDenseGate ? 64 : 128;
   const int most = num_sms / 2;
   Plan best{};
-  double best_t;
+  double best_t, bytes = 0.0;
   {
     int64_t tiles = 0;
     double work = 0.0, longest = 0.0;
     for (int i = 0; i < n; ++i) {
       const int64_t t = ((p[i].M + 255) / 256) * ((p[i].N + oc - 1) / oc);
+      const double M = static_cast<double>(p[i].M), N = static_cast<double>(p[i].N), K = static_cast<double>(p[i].K);
       const double nk = static_cast<double>((p[i].K + 63) / 64);
       tiles += t;
       work += static_cast<double>(t) * nk;
       longest = nk > longest ? nk : longest;
+      bytes += 2.0 * (M * K + N * K * (EPI == kDenseGate ? 2 : 1) +
+                      M * N * (EPI == kDenseGateGrad ? 5 : p[i].residual != nullptr ? 2 : 1));
     }
+    if (tiles > 4 * most) return best;  // large: the pair kernel's
     if (n == 1) {
       const int64_t rest = tiles % most;
       const bool cut = 2 * rest <= most;
       const int64_t rounds = cut ? tiles / most : (tiles + most - 1) / most;
-      best_t = kPairStart + longest * (kPairStep * static_cast<double>(rounds) + (cut && rest ? kHalfStep : 0.0));
+      best_t = longest * (kPairStep * static_cast<double>(rounds) + (cut && rest ? kHalfStep : 0.0)) +
+               (rounds ? kPairEnd : 0.0);
     } else {
       const double even = work / most + 0.5 * longest;
-      best_t = kPairStart + kPairStep * (even > longest ? even : longest);
+      best_t = kPairStep * (even > longest ? even : longest) + kPairEnd;
     }
-    if (tiles > 4 * most) return best;  // large: the pair kernel's
+    if (best_t < bytes / kPairHbm) best_t = bytes / kPairHbm;
+    best_t += kPairStart;
   }
   for (int bt = MAJOR == kMajorAny ? 64 : 16; bt <= 128; bt *= 2) {
     const int64_t slots = static_cast<int64_t>(num_sms) * (bt <= 64 ? 2 : 1);
@@ -510,24 +521,28 @@ Plan plan_of(const DenseProblem* p, int n, int num_sms) {
       // the first m jobs (those of the longest contraction) in s parts
       for (int m = s == 1 ? 0 : 1; m <= (s == 1 ? 0 : n); ++m) {
         int64_t ctas = 0;
-        for (int i = 0; i < n; ++i)
-          ctas += ((p[i].M + bt - 1) / bt) * ((p[i].N + so - 1) / so) * (i < m ? s : 1);
-        const double live = static_cast<double>(ctas < slots ? ctas : slots);
-        double step = live * (16384 + bt * 128) / kL2;
+        double tiles[kMaxJobs];
+        for (int i = 0; i < n; ++i) {
+          const int64_t t = ((p[i].M + bt - 1) / bt) * ((p[i].N + so - 1) / so) * (i < m ? s : 1);
+          ctas += t;
+          tiles[i] = static_cast<double>(t);
+        }
+        double step = static_cast<double>(ctas < slots ? ctas : slots) * (16384 + bt * 128) / kFill;
         if (step < kStep) step = kStep;
         double total = 0.0, longest = 0.0;
         for (int i = 0; i < n; ++i) {
           const int k = i < m ? s : 1;
-          const double tiles = static_cast<double>(((p[i].M + bt - 1) / bt) * ((p[i].N + so - 1) / so) * k);
           const double rows = static_cast<double>(p[i].M < bt ? p[i].M : bt) * (EPI == kDenseGateGrad ? 2 : 1);
           const double t = static_cast<double>((p[i].K + 64 * k - 1) / (64 * k)) * step + kRow * rows / k +
-                           (k > 1 ? kJoin * k : 0.0);
-          total += tiles * t;
+                           (k > 1 ? kJoin * k : 0.0) + (bt == 128 ? kTall : 0.0);
+          total += tiles[i] * t;
           longest = t > longest ? t : longest;
         }
         double t = total / static_cast<double>(slots);
         if (t < longest) t = longest;
-        t += kStart + (ctas > slots ? kRound : 0.0);
+        if (ctas > slots) t += kRound;
+        if (t < bytes / kHbm) t = bytes / kHbm;
+        t += kStart;
         if (t < best_t) {
           best_t = t;
           best.split = true;

@@ -117,12 +117,37 @@ __device__ __forceinline__ F2 gelu_tanh_gate(F2 z, F2 z2) {
   return rcp_1p_exp2(z * fma2(z2, f2(c * kGeluCubic), f2(c)));
 }
 
-// act(z).  NaN stays NaN.  gelu goes through erfc, which keeps its relative
-// precision for negative z.
+// gelu: the normal distribution Phi(z), by Abramowitz and Stegun 7.1.26 (a
+// polynomial in 1 / (1 + p x) times e^-x^2 with x = |z| / sqrt 2; Phi within
+// 7.5e-8), and e^(-z^2 / 2), which its density needs too.
+__device__ __forceinline__ F2 normal_cdf(F2 z, F2* e) {
+  const F2 x = each(z, [](float v) { return fabsf(v); }) * f2(kSqrtHalf);
+  const F2 t = each(fma2(x, f2(0.3275911f), f2(1.0f)), [](float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+  });
+  *e = each(z * z * f2(-0.5f * kLog2E), [](float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+  });
+  F2 q = fma2(t, f2(0.5f * 1.061405429f), f2(0.5f * -1.453152027f));
+  q = fma2(t, q, f2(0.5f * 1.421413741f));
+  q = fma2(t, q, f2(0.5f * -0.284496736f));
+  q = fma2(t, q, f2(0.5f * 0.254829592f));
+  const float2 tail = split(q * t * *e), s = split(z);  // Phi(-|z|)
+  return f2(s.x < 0.0f ? tail.x : 1.0f - tail.x, s.y < 0.0f ? tail.y : 1.0f - tail.y);
+}
+
+// act(z).  NaN stays NaN.
 template <int ACT>
 __device__ __forceinline__ F2 act_value(F2 z) {
   if constexpr (ACT == MOE_EPI_SILU) return z * silu_gate(z);
-  if constexpr (ACT == MOE_EPI_GELU) return each(z, [](float x) { return 0.5f * x * erfcf(-kSqrtHalf * x); });
+  if constexpr (ACT == MOE_EPI_GELU) {
+    F2 e;
+    return z * normal_cdf(z, &e);
+  }
   if constexpr (ACT == MOE_EPI_GELU_TANH) return z * gelu_tanh_gate(z, square_to_400(z));
   if constexpr (ACT == MOE_EPI_RELU || ACT == MOE_EPI_RELU2) {
     const F2 p = each(z, [](float x) { return x < 0.0f ? 0.0f : x; });
@@ -140,11 +165,11 @@ __device__ __forceinline__ F2 act_value_slope(F2 z, F2* slope) {
     return v;
   }
   if constexpr (ACT == MOE_EPI_GELU) {
-    const F2 phi = each(z, [](float x) { return 0.5f * erfcf(-kSqrtHalf * x); });
-    *slope = phi + each(z, [](float x) {
-               const float c = fminf(fmaxf(x, -20.0f), 20.0f);  // beyond, the density is 0
-               return c * kInvSqrt2Pi * __expf(-0.5f * c * c);
-             });
+    F2 e;
+    const F2 phi = normal_cdf(z, &e);
+    // z times the density; where e is 0 an infinite z must not meet it
+    const F2 zc = each(z, [](float x) { return fminf(fmaxf(x, -20.0f), 20.0f); });
+    *slope = fma2(zc * f2(kInvSqrt2Pi), e, phi);
     return z * phi;
   }
   if constexpr (ACT == MOE_EPI_GELU_TANH) {
