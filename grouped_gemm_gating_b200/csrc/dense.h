@@ -79,7 +79,7 @@ struct ClipEntry {
   int64_t first;   // index of the tensor's first chunk
   int64_t dtype;   // moe_dtype
 };
-constexpr int kClipMaxBlocks = 2048;
+constexpr int kClipMaxBlocks = 1024;
 cudaError_t launch_clip_plan(const ClipEntry* entries, int n, ClipEntry* plan, cudaStream_t stream, int* launches);
 // partial: kClipMaxBlocks doubles; norm: one float.
 cudaError_t launch_clip_norm(const ClipEntry* plan, int n, int64_t chunks, int norm_type, double* partial, float* norm,

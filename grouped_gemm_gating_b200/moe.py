@@ -411,6 +411,7 @@ def moe_layer_fp8(logits, x, wq: Fp8Experts, k, block_m, act, topk_ids, topk_wei
 # comparison per tensor, with the reason worked out only when it fails.
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _stream_of(index):
@@ -430,9 +431,15 @@ def _rows(fn, name, t, T, cols, dtype, index):
     None -> (None, 0)."""
     if t is None:
         return None, 0
-    if t.shape != (T, cols) or t.dtype is not dtype or t.get_device() != index or (t.stride(1) != 1 and cols > 1):
+    if t.shape != (T, cols) or t.dtype is not dtype or t.get_device() != index:
         _refuse(fn, name, t, (T, cols), dtype, index)
-    return t.data_ptr(), t.stride(0) if T > 1 else max(cols, 8)
+    if t.is_contiguous() or T < 2:
+        if T == 1 and cols > 1 and t.stride(1) != 1:
+            _refuse(fn, name, t, (T, cols), dtype, index)
+        return t.data_ptr(), cols
+    if t.stride(1) != 1:
+        _refuse(fn, name, t, (T, cols), dtype, index)
+    return t.data_ptr(), t.stride(0)
 
 
 def _whole(fn, name, t, shape, dtype, index):
@@ -471,7 +478,7 @@ def _call(fn, index, *args):
     """Calls the library on the current stream of the device (the last
     argument) with that device current."""
     f = getattr(_lib or load_library(), fn)
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:
         code = f(*args, _stream_of(index))
     else:
         with torch.cuda.device(index):
