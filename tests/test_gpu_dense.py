@@ -44,6 +44,11 @@ LINEAR = [
     (777, 1000, 1848, "relu2", True, True, True, HF, 24),
     (1100, 520, 2312, "gelu_tanh", True, True, True, BF, 0),
     (2500, 72, 1032, "none", True, True, False, BF, 8),
+    # several rounds of tiles: a whole last round, halves in it, and a last
+    # column of tiles that lies half outside
+    (5003, 136, 2552, "silu", True, True, False, BF, 8),
+    (4700, 200, 2048, "none", False, True, True, HF, 0),
+    (9700, 64, 1304, "gelu_tanh", True, False, True, BF, 0),
 ]
 
 
@@ -130,6 +135,7 @@ LINEAR_BWD = [
     (413, 1352, 680, "none", True, False, HF, 8),
     (300, 72, 1032, "relu", True, True, BF, 0),
     (1030, 520, 264, "silu", True, False, BF, 40),
+    (4700, 1024, 5112, "none", False, True, BF, 8),   # rounds of tiles, both products in one launch
 ]
 
 
@@ -186,6 +192,8 @@ FFN = [
     (261, 672, 464, "gelu", False, True, BF, 0),
     (300, 1016, 1720, "none", True, True, HF, 0),
     (1290, 136, 328, "silu", True, False, BF, 8),
+    (5003, 72, 1256, "silu", True, True, BF, 8),      # rounds of tiles
+    (4900, 200, 1000, "gelu", False, False, HF, 0),
 ]
 
 
