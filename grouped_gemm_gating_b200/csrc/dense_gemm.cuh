@@ -29,8 +29,8 @@
 // epilogue's transfers are whole 128-byte lines (8192 x 6144 x 2048, dh with
 // [dg | du] and h: a thread per row 220 us, 64-byte rows by TMA 195 us).
 //
-// Tiles go in groups of kGroupM row tiles, column by column, so the pairs at
-// work share operand rows in L2.  The tiles that do not fill a last round of
+// Tiles go in groups of row tiles (group_rows), so the pairs at work share
+// operand rows in L2.  The tiles that do not fill a last round of
 // all pairs are cut into halves of BN / 2 columns when that shortens it.
 //
 // Every mbarrier wait is bounded; on expiry the CTA records
@@ -52,7 +52,13 @@ namespace dense {
 // After an abort, the odd CTA's wait for its last loads to land (they
 // complete on the even CTA's barriers): far above a TMA load's latency.
 constexpr uint64_t kDrainGraceNs = 50000;
-constexpr int kGroupM = 8;
+
+// Row tiles of a group: tiles go column by column within it.  The shorter
+// side of the grid of tiles is kept whole, so that its operand stays in L2
+// and the other one passes once (measured with groups of 2, 8 and 16: 64 x 8
+// tiles at K = 8192 352, 359 and 368 us, a gate of 16 x 96 at K = 4096 585,
+// 514 and 502 us, 32 x 32 at K = 8192 763, 693 and 720 us).
+inline int group_rows(int n_mt, int n_nt) { return n_nt <= 8 ? 2 : n_mt <= 16 ? 16 : 8; }
 
 struct Job {
   CUtensorMap tm_a, tm_b;
@@ -60,7 +66,7 @@ struct Job {
   CUtensorMap tm_out, tm_pre;    // out and pre; gate-grad: da and h
   CUtensorMap tm_res;            // residual; gate-grad: [g | u]
   int64_t M, N;
-  int nk, n_mt, n_nt;
+  int nk, n_mt, n_nt, group;
   int a_mn, b_mn;                // kMajorAny
   const uint16_t* bias;
   int residual, keep_pre;        // tm_res, tm_pre are wanted
@@ -193,10 +199,10 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
       if (j < args.n_jobs && tile >= args.tile0[j]) r.job = j;
     const Job& jb = args.job[r.job];
     if (C::kJobs > 1) tile -= args.tile0[r.job];
-    const int per_group = kGroupM * jb.n_nt;
+    const int per_group = jb.group * jb.n_nt;
     const int g = tile / per_group;
-    const int m0 = g * kGroupM;
-    const int gm = jb.n_mt - m0 < kGroupM ? jb.n_mt - m0 : kGroupM;
+    const int m0 = g * jb.group;
+    const int gm = jb.n_mt - m0 < jb.group ? jb.n_mt - m0 : jb.group;
     const int i = tile - g * per_group;
     r.nt = i / gm;
     r.mt = m0 + (i - r.nt * gm);
@@ -696,6 +702,7 @@ bool make_job(const DenseProblem& p, Job* a) {
   a->nk = static_cast<int>((p.K + 63) / 64);
   a->n_mt = static_cast<int>((p.M + 255) / 256);
   a->n_nt = static_cast<int>((p.N + C::kOutCols - 1) / C::kOutCols);
+  a->group = group_rows(a->n_mt, a->n_nt);
   a->bias = static_cast<const uint16_t*>(p.bias);
   return ok;
 }
