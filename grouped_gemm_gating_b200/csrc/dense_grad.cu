@@ -19,10 +19,12 @@ constexpr int kCols = 64;
 constexpr int kThreads = 256;
 constexpr int kRows = kThreads / 8;  // rows of a block's step
 constexpr int kParts = 8;
+// Rows of a thread in flight, and four blocks an SM (64 registers): 8192 x 8192
+// with silu 79 us, 5.1 TB/s; three blocks 88 us, two blocks with four rows 87.
 constexpr int kUnroll = 2;
 
 template <bool kFp16>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, 4)
     dz_kernel(const uint16_t* dout, int64_t ldd, const uint16_t* pre, int64_t ldp, int64_t T, int64_t N, int act,
               uint16_t* dz, uint16_t* dbias) {
   __shared__ float sums[kThreads / kWarp][kCols];
