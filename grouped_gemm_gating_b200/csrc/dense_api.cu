@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <cstdlib>
 #include <initializer_list>
 
 #include "../../include/moe.h"
@@ -114,6 +115,37 @@ DenseProblem gradient(int major, moe_dtype dtype, int64_t M, int64_t N, int64_t 
   p.ldo = ldo;
   p.status = status;
   return p;
+}
+
+// Whether a target shares memory with another tensor's source or target, or
+// its own source shifted.  Intervals sorted by their start; a failed
+// allocation reports -1.
+struct Interval {
+  uintptr_t start, end;
+  bool target;
+};
+int targets_overlap(const void* const* src, void* const* dst, const int64_t* numel, const int32_t* dtype, int n) {
+  Interval* v = static_cast<Interval*>(std::malloc(2 * static_cast<size_t>(n) * sizeof(Interval)));
+  if (v == nullptr) return -1;
+  int m = 0;
+  for (int i = 0; i < n; ++i) {
+    if (numel[i] == 0) continue;
+    const uintptr_t bytes = static_cast<uintptr_t>(numel[i]) * (dtype[i] == MOE_FP32 ? 4 : 2);
+    const uintptr_t s = reinterpret_cast<uintptr_t>(src[i]);
+    const uintptr_t d = dst != nullptr ? reinterpret_cast<uintptr_t>(dst[i]) : s;
+    v[m++] = {d, d + bytes, true};
+    if (s != d) v[m++] = {s, s + bytes, false};
+  }
+  std::sort(v, v + m, [](const Interval& a, const Interval& b) { return a.start < b.start; });
+  uintptr_t target_end = 0, source_end = 0;
+  int found = 0;
+  for (int i = 0; i < m && !found; ++i) {
+    found = v[i].start < target_end || (v[i].target && v[i].start < source_end);
+    uintptr_t* end = v[i].target ? &target_end : &source_end;
+    if (v[i].end > *end) *end = v[i].end;
+  }
+  std::free(v);
+  return found;
 }
 
 // One launch for all of them, the longest contraction first.
@@ -416,11 +448,10 @@ moe_status moe_grad_plan(const void* const* src, void* const* dst, const int64_t
     const uintptr_t size = dtype[i] == MOE_FP32 ? 4 : 2;
     const uintptr_t s = reinterpret_cast<uintptr_t>(src[i]);
     const uintptr_t d = dst != nullptr ? reinterpret_cast<uintptr_t>(dst[i]) : s;
-    const uintptr_t bytes = static_cast<uintptr_t>(numel[i]) * size;
     if (s == 0 || d == 0 || s % size || d % size) return MOE_ERR_INVALID_ARG;
-    if (s != d && s < d + bytes && d < s + bytes) return MOE_ERR_INVALID_ARG;  // shifted onto itself
     total += (numel[i] + moe::kClipChunk - 1) / moe::kClipChunk;
   }
+  if (targets_overlap(src, dst, numel, dtype, n) != 0) return MOE_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int launches = 0;
   int64_t first = 0;

@@ -664,14 +664,16 @@ class GradClip:
         self.chunks = chunks.value
 
     def norm(self, norm_type=NORM_L2):
-        """The global norm (a 0-d fp32 tensor on the device)."""
+        """The global norm (a 0-d fp32 tensor on the device, rewritten by the
+        next call)."""
         _call("moe_grad_norm", self.index, self.plan.data_ptr(), self.n, self.chunks, norm_type,
               self.total_norm.data_ptr(), self.ws.data_ptr(), self.ws.numel(), self.status.data_ptr())
         return self.total_norm
 
     def clip(self, max_norm, norm_type=NORM_L2):
         """Scales the gradients to a global norm of at most max_norm; returns
-        the norm before (a 0-d fp32 tensor on the device)."""
+        the norm before (a 0-d fp32 tensor on the device, rewritten by the
+        next call)."""
         _call("moe_grad_clip", self.index, self.plan.data_ptr(), self.n, self.chunks, norm_type, float(max_norm),
               self.total_norm.data_ptr(), self.ws.data_ptr(), self.ws.numel(), self.status.data_ptr())
         return self.total_norm

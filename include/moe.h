@@ -544,8 +544,9 @@ MOE_API moe_status moe_ffn_backward(const uint16_t* x, int64_t ldx, int64_t T, i
  *   src, numel, dtype  host arrays of n device pointers, element counts and
  *                      moe_dtype values.
  *   dst                host array of n targets, or NULL: in place.  A target
- *                      is its source or does not overlap it, and no target
- *                      overlaps another tensor (not checked across tensors).
+ *                      is its source or overlaps no source, and no target
+ *                      overlaps another (so no tensor is listed twice in
+ *                      place): MOE_ERR_INVALID_ARG.
  * MOE_ERR_WORKSPACE if the plan buffer is missing or too small.
  */
 typedef enum { MOE_NORM_L2 = 0, MOE_NORM_MAX = 1 } moe_norm_type;

@@ -174,6 +174,11 @@ def test_grad_plan_checks(lib):
     assert plan(lib, [GiB + 2], [8], [2]) == INVALID
     assert plan(lib, [GiB], [8], [0], dst=[GiB + 8]) == INVALID           # shifted onto itself
     assert plan(lib, [GiB], [8], [0], dst=[None]) == INVALID
+    assert plan(lib, [GiB, GiB], [8, 8], [0, 0]) == INVALID               # the same tensor twice, in place
+    assert plan(lib, [GiB, GiB + 8], [8, 8], [0, 0]) == INVALID           # views that overlap
+    assert plan(lib, [GiB, 2 * GiB], [8, 8], [0, 0], dst=[3 * GiB, 3 * GiB + 14]) == INVALID
+    assert plan(lib, [GiB, 2 * GiB], [8, 8], [0, 0], dst=[3 * GiB, GiB]) == INVALID   # a target on another's source
+    assert plan(lib, [2 * GiB, GiB], [8, (1 << 28) + 4], [0, 2], dst=[3 * GiB, GiB]) == INVALID  # in another target
     assert plan(lib, [GiB], [8], [0], plan_p=None) == WORKSPACE
     assert plan(lib, [GiB], [8], [0], plan_b=16) == WORKSPACE
     assert plan(lib, [GiB], [8], [0], plan_p=ctypes.c_void_p(GiB + 8)) == WORKSPACE

@@ -91,6 +91,29 @@ def test_norm_of_tiny_and_large_gradients(std, dtype):
     check_clip(grads, plan._held[1], plan, 1.0)
 
 
+def test_no_elements():
+    grads = [torch.empty(0, dtype=BF, device="cuda"), torch.empty((3, 0), device="cuda")]
+    plan = M.GradClip(grads)
+    assert float(plan.clip(1.0)) == 0.0 and float(plan.norm()) == 0.0
+    assert M.moe_read_status(plan.status) == 0
+
+
+def test_one_source_for_two_targets():
+    g = tensors([3000], (FP,), 8)[0]
+    a, b = torch.empty_like(g), torch.empty_like(g)
+    check_clip([g, g], [a, b], M.GradClip([g, g], [a, b]), 1.0)
+
+
+def test_more_elements_than_32_bits_count():
+    """2^31 + 5 bf16 values: the last ones are counted and scaled."""
+    g = torch.zeros((1 << 31) + 5, dtype=BF, device="cuda")
+    g[-3:] = 2.0
+    g[0] = 2.0
+    plan = M.GradClip([g])
+    assert abs(float(plan.clip(1.0)) - 4.0) <= 1e-6
+    assert g[-3:].tolist() == [0.5] * 3 and float(g[0]) == 0.5 and float(g[1 << 30]) == 0.0
+
+
 def test_zero_gradients():
     grads = [torch.zeros(5000, dtype=BF, device="cuda"), torch.zeros(3, device="cuda")]
     plan = M.GradClip(grads)
@@ -141,7 +164,8 @@ def test_same_on_every_call_and_in_a_graph():
 def test_refusals():
     a = torch.zeros(100, device="cuda")
     for grads, outs in (([a.to(torch.float64)], None), ([a[::2]], None), ([a], [a[:50]]), ([a], [a.to(BF)]),
-                        ([a], [a.cpu()]), ([a[:50]], [a[1:51]])):
+                        ([a], [a.cpu()]), ([a[:50]], [a[1:51]]), ([a, a], None),
+                        ([a[:60], a[50:]], None)):
         with pytest.raises((ValueError, M.MoEError)):
             M.GradClip(grads, outs)
     plan = M.GradClip([a])

@@ -381,26 +381,96 @@ def test_offsets_past_32_bits():
     assert torch.equal(out[:5], (x[:5].float() @ w.float().T).to(BF))
 
 
-@pytest.mark.parametrize("T", [4, 300])
-def test_timeout_is_reported(T):
-    """A wait that runs out sets the status; the next call works."""
+@pytest.mark.parametrize("T,N", [(4, 512), (300, 512), (9000, 2048)])
+def test_timeout_is_reported(T, N):
+    """A wait that runs out sets the status; the next call works.  Few rows,
+    a medium batch, and the pair kernel with a residual on its way."""
     d = Draw(41, BF)
-    x, w = d.whole((T, 512)), d.whole((512, 512), 0.05)
-    want, out = torch.empty(T, 512, dtype=BF, device="cuda"), torch.empty(T, 512, dtype=BF, device="cuda")
+    x, w, r = d.whole((T, 512)), d.whole((N, 512), 0.05), d.whole((T, N))
+    want, out = torch.empty(T, N, dtype=BF, device="cuda"), torch.empty(T, N, dtype=BF, device="cuda")
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
-    M.moe_linear(x, w, want, dev_status=status)
+    M.moe_linear(x, w, want, None, r, dev_status=status)
     ok(status)
     try:
         M.moe_debug_timeouts(20_000_000, 1)
-        M.moe_linear(x, w, out, dev_status=status)
+        M.moe_linear(x, w, out, None, r, dev_status=status)
         torch.cuda.synchronize()
     finally:
         M.moe_debug_timeouts(0, 0)
     assert M.status_name(M.moe_read_status(status)) == "MOE_ERR_DEVICE_TIMEOUT"
     status.zero_()
-    M.moe_linear(x, w, out, dev_status=status)
+    M.moe_linear(x, w, out, None, r, dev_status=status)
     ok(status)
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("T", [40, 9000])
+def test_timeout_in_the_block(T):
+    """The same through moe_ffn and moe_ffn_backward (gate, gate gradient and
+    joint gradient kernels)."""
+    d = Draw(42, BF)
+    dd, F = 512, 1024
+    x, w13, w2, dout = d.whole((T, dd)), d.whole((2 * F, dd), 0.05), d.whole((dd, F), 0.05), d.whole((T, dd))
+    b = M.FFNBuffers(T, dd, F, train=True)
+
+    def step():
+        b.forward(x, w13, w2, x)
+        b.backward(x, w13, w2, dout, dx_residual=dout)
+        torch.cuda.synchronize()
+        return [t.clone() for t in (b.out, b.dx, b.dw13, b.dw2)]
+
+    want = step()
+    ok(b.status)
+    try:
+        M.moe_debug_timeouts(10_000_000, 1)
+        step()
+    finally:
+        M.moe_debug_timeouts(0, 0)
+    assert M.status_name(M.moe_read_status(b.status)) == "MOE_ERR_DEVICE_TIMEOUT"
+    b.status.zero_()
+    for a, c in zip(step(), want):
+        assert torch.equal(a, c)
+    ok(b.status)
+
+
+@pytest.mark.parametrize("T", [3, 700, 6000])
+def test_slices_of_one_buffer(T):
+    """x and out are neighbouring column slices of one buffer."""
+    d = Draw(43, BF)
+    buf = d.whole((T, 200 + 1000))
+    keep = buf[:, :200].clone()
+    w = d.whole((1000, 200), 0.1)
+    want = torch.empty(T, 1000, dtype=BF, device="cuda")
+    M.moe_linear(keep, w, want)
+    M.moe_linear(buf[:, :200], w, buf[:, 200:])
+    torch.cuda.synchronize()
+    assert torch.equal(buf[:, 200:], want) and torch.equal(buf[:, :200], keep)
+
+
+def test_two_calls_at_once():
+    """Two streams run the block on buffers of their own at the same time."""
+    d = Draw(44, BF)
+    dd, F = 264, 520
+    w13, w2 = d.whole((2 * F, dd), 0.1), d.whole((dd, F), 0.1)
+    xs = [d.whole((T, dd)) for T in (5, 900)]
+    bufs = [M.FFNBuffers(x.shape[0], dd, F, train=True) for x in xs]
+    want = []
+    for x, b in zip(xs, bufs):
+        b.forward(x, w13, w2)
+        b.backward(x, w13, w2, x)
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in (b.out, b.dx, b.dw13, b.dw2)])
+    streams = [torch.cuda.Stream() for _ in xs]
+    for _ in range(20):
+        for x, b, s in zip(xs, bufs, streams):
+            with torch.cuda.stream(s):
+                b.forward(x, w13, w2)
+                b.backward(x, w13, w2, x)
+    torch.cuda.synchronize()
+    for b, ref in zip(bufs, want):
+        for t, r in zip((b.out, b.dx, b.dw13, b.dw2), ref):
+            assert torch.equal(t, r)
+        ok(b.status)
 
 
 def test_refusals_leave_outputs_alone():
