@@ -23,11 +23,12 @@
 // columns at a time.  Matrices move between shared and global memory by TMA
 // only, a warp of each group moving them: it fetches what the next chunks add
 // (a residual, or g and u) as soon as the buffers' last results have left,
-// and stores what the group has written in their place.  What bounds the
-// kernel is what an SM takes in (64 bytes a clock, and about 11 TB/s from L2
-// for all): a 64-wide K step brings 32 KB for 512 clocks of products, so the
-// epilogue's transfers are whole 128-byte lines (8192 x 6144 x 2048, dh with
-// [dg | du] and h: a thread per row 220 us, 64-byte rows by TMA 195 us).
+// and stores what the group has written in their place.  A step of 64 of k
+// brings each SM 32 KB for 512 clocks of products, so other traffic adds to
+// the products' time instead of hiding under it: 8192 x 6144 x 2048 takes
+// 134 us as a plain product; dh with [dg | du] and h, 0.5 GB more, 206 us
+// (timing-only builds without its loads 173 us, without its stores 154 us,
+// without both 126 us; a thread per row instead of TMA 220 us).
 //
 // Tiles go in groups of row tiles (group_rows), so the pairs at work share
 // operand rows in L2.  The tiles that do not fill a last round of

@@ -480,7 +480,10 @@ Plan plan_of(const DenseProblem* p, int n, int num_sms) {
   constexpr double kPairEnd = 1.1, kPairHbm = 3.65e6;
   // here: launch to last store, 64 of k, stages' bytes of all SMs, a row's and a part's epilogue, 128-row tiles
   // (one CTA an SM), a second round of CTAs
-  constexpr double kStart = 4.07, kStep = 0.154, kFill = 12.2e6, kHbm = 8.6e6;
+  constexpr double kStart = 4.07, kStep = 0.154, kFill = 12.2e6;
+  // weights from memory, and what one CTA streams: 134 MB at three rows in
+  // 26.4 us by 128 CTAs, 23.9 us by 256; 67 MB in 18.8 us by 64, 14.5 by 128
+  constexpr double kHbmFew = 6.0e6, kHbm = 6.7e6, kHbmCta = 0.055e6;
   constexpr double kRow = 0.0081, kJoin = 0.154, kTall = 1.26, kRound = 3.2;
   const int oc = EPI == kDenseGate ? 128 : 256, so = EPI == kDenseGate ? 64 : 128;
   const int most = num_sms / 2;
@@ -527,6 +530,7 @@ Plan plan_of(const DenseProblem* p, int n, int num_sms) {
           ctas += t;
           tiles[i] = static_cast<double>(t);
         }
+        if (ctas > 2 * slots) continue;  // many tiles: the pair kernel's
         double step = static_cast<double>(ctas < slots ? ctas : slots) * (16384 + bt * 128) / kFill;
         if (step < kStep) step = kStep;
         double total = 0.0, longest = 0.0;
@@ -541,7 +545,9 @@ Plan plan_of(const DenseProblem* p, int n, int num_sms) {
         double t = total / static_cast<double>(slots);
         if (t < longest) t = longest;
         if (ctas > slots) t += kRound;
-        if (t < bytes / kHbm) t = bytes / kHbm;
+        double rate = ctas > num_sms ? kHbm : kHbmFew;
+        if (rate > kHbmCta * static_cast<double>(ctas)) rate = kHbmCta * static_cast<double>(ctas);
+        if (t < bytes / rate) t = bytes / rate;
         t += kStart;
         if (t < best_t) {
           best_t = t;

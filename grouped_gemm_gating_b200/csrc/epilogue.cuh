@@ -11,9 +11,9 @@
 namespace moe {
 
 // Two fp32 values in a register pair; sm_100a adds, multiplies and fuses both
-// in one instruction.  An epilogue's arithmetic is what bounds it (measured:
-// 37 scalar instructions an element held dh with its gate gradient at 19 us a
-// tile of 256 x 256 whose products take 10).
+// in one instruction.  An epilogue has few warps beside the product's own, so
+// its instructions count (dz at 8192 x 8192 with tanh-gelu: 120 us one value
+// at a time, 91 us two).
 struct F2 {
   uint64_t v;
 };
