@@ -47,12 +47,13 @@ struct DenseProblem {
   int b_ready;           // b is not written by the kernel before this one in the stream
   int32_t* status;
 };
-cudaError_t launch_dense_linear(const DenseProblem& p, int num_sms, cudaStream_t stream);
-cudaError_t launch_dense_gate(const DenseProblem& p, int num_sms, cudaStream_t stream);
-cudaError_t launch_dense_gate_grad(const DenseProblem& p, int num_sms, cudaStream_t stream);
+cudaError_t launch_dense_linear(const DenseProblem& p, int num_sms, cudaStream_t stream, int* launches);
+cudaError_t launch_dense_gate(const DenseProblem& p, int num_sms, cudaStream_t stream, int* launches);
+cudaError_t launch_dense_gate_grad(const DenseProblem& p, int num_sms, cudaStream_t stream, int* launches);
 // Up to kMaxJobs independent kMajorKN / kMajorMN products (gradients: no
-// bias, activation or pre) in one launch.
-cudaError_t launch_dense_grads(const DenseProblem* p, int n, int num_sms, cudaStream_t stream);
+// bias, activation or pre), the longest contraction first, in one launch or
+// two.
+cudaError_t launch_dense_grads(const DenseProblem* p, int n, int num_sms, cudaStream_t stream, int* launches);
 
 // dz = dout * act'(pre) (pre null: dz is dout and is not written) and, with
 // dbias, dbias[n] = sum_t dz[t, n].

@@ -152,7 +152,8 @@ int targets_overlap(const void* const* src, void* const* dst, const int64_t* num
 moe_status launch_gradients(DenseProblem* jobs, int n, int sms, cudaStream_t s, int launches) {
   if (n == 0) return finish(cudaSuccess, launches);
   std::sort(jobs, jobs + n, [](const DenseProblem& a, const DenseProblem& b) { return a.K > b.K; });
-  return finish(moe::launch_dense_grads(jobs, n, sms, s), launches + 1);
+  const cudaError_t err = moe::launch_dense_grads(jobs, n, sms, s, &launches);
+  return finish(err, launches);
 }
 
 Mat ws_mat(void* ws, size_t bytes) {  // the workspace as one row, for the overlap checks
@@ -203,7 +204,9 @@ moe_status moe_linear(const uint16_t* x, int64_t ldx, int64_t T, int K, const ui
   p.status = dev_status;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   StageScope scope(kStLinear, s);
-  return finish(moe::launch_dense_linear(p, sms, s), 1);
+  int launches = 0;
+  const cudaError_t err = moe::launch_dense_linear(p, sms, s, &launches);
+  return finish(err, launches);
 }
 
 size_t moe_linear_backward_workspace_size(int64_t T, int K, int N, moe_epi_act act) {
@@ -324,9 +327,10 @@ moe_status moe_ffn(const uint16_t* x, int64_t ldx, int64_t T, int d, const uint1
   p.ldp = F2;
   p.status = dev_status;
   cudaError_t err;
+  int launches = 0;
   {
     StageScope scope(kStFfnGate, s);
-    err = moe::launch_dense_gate(p, sms, s);
+    err = moe::launch_dense_gate(p, sms, s, &launches);
   }
   if (err != cudaSuccess) return MOE_ERR_CUDA;
   p.epi = moe::kDenseLinear;
@@ -345,9 +349,9 @@ moe_status moe_ffn(const uint16_t* x, int64_t ldx, int64_t T, int d, const uint1
   p.pre = nullptr;
   {
     StageScope scope(kStLinear, s);
-    err = moe::launch_dense_linear(p, sms, s);
+    err = moe::launch_dense_linear(p, sms, s, &launches);
   }
-  return finish(err, 2);
+  return finish(err, launches);
 }
 
 size_t moe_ffn_backward_workspace_size(int64_t T, int d, int F) {
@@ -416,9 +420,8 @@ moe_status moe_ffn_backward(const uint16_t* x, int64_t ldx, int64_t T, int d, co
   p.pre = const_cast<uint16_t*>(pre);
   p.ldp = F2;
   p.out2 = h;
-  err = moe::launch_dense_gate_grad(p, sms, s);
+  err = moe::launch_dense_gate_grad(p, sms, s, &launches);
   if (err != cudaSuccess) return MOE_ERR_CUDA;
-  ++launches;
   DenseProblem jobs[3];
   int n = 0;
   if (dx) {

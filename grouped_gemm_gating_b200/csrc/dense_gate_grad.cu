@@ -2,8 +2,8 @@
 
 namespace moe {
 
-cudaError_t launch_dense_gate_grad(const DenseProblem& p, int num_sms, cudaStream_t stream) {
-  return dense::launch_kind<kDenseGateGrad, kMajorKN>(&p, 1, num_sms, stream);
+cudaError_t launch_dense_gate_grad(const DenseProblem& p, int num_sms, cudaStream_t stream, int* launches) {
+  return dense::launch_kind<kDenseGateGrad, kMajorKN>(&p, 1, num_sms, stream, launches);
 }
 
 }  // namespace moe

@@ -471,6 +471,7 @@ struct Plan {
   bool split;
   int bt, s;            // rows of a tile, CTAs of a cluster
   int parts[kMaxJobs];  // parts of k: s or 1
+  double us;            // estimate
 };
 
 template <int EPI, int MAJOR>
@@ -502,7 +503,6 @@ Plan plan_of(const DenseProblem* p, int n, int num_sms) {
       bytes += 2.0 * (M * K + N * K * (EPI == kDenseGate ? 2 : 1) +
                       M * N * (EPI == kDenseGateGrad ? 5 : p[i].residual != nullptr ? 2 : 1));
     }
-    if (tiles > 4 * most) return best;  // large: the pair kernel's
     if (n == 1) {
       const int64_t rest = tiles % most;
       const bool cut = 2 * rest <= most;
@@ -515,6 +515,8 @@ Plan plan_of(const DenseProblem* p, int n, int num_sms) {
     }
     if (best_t < bytes / kPairHbm) best_t = bytes / kPairHbm;
     best_t += kPairStart;
+    best.us = best_t;
+    if (tiles > 4 * most) return best;  // large: the pair kernel's
   }
   for (int bt = MAJOR == kMajorAny ? 64 : 16; bt <= 128; bt *= 2) {
     const int64_t slots = static_cast<int64_t>(num_sms) * (bt <= 64 ? 2 : 1);
@@ -560,17 +562,38 @@ Plan plan_of(const DenseProblem* p, int n, int num_sms) {
     }
     if (!more) break;
   }
+  best.us = best_t;
   return best;
 }
 
 template <int EPI, int MAJOR>
-cudaError_t launch_kind(const DenseProblem* p, int n, int num_sms, cudaStream_t stream) {
-  const Plan plan = plan_of<EPI, MAJOR>(p, n, num_sms);
+cudaError_t launch_planned(const DenseProblem* p, int n, const Plan& plan, int num_sms, cudaStream_t stream) {
   if (plan.split)
     return p->fp16 ? launch_split<EPI, MAJOR, true>(p, n, plan.bt, plan.s, plan.parts, stream)
                    : launch_split<EPI, MAJOR, false>(p, n, plan.bt, plan.s, plan.parts, stream);
   return p->fp16 ? launch_pair<EPI, MAJOR, true>(p, n, num_sms, stream)
                  : launch_pair<EPI, MAJOR, false>(p, n, num_sms, stream);
+}
+
+// One launch, or two where that saves more than a launch costs the host: the
+// first job alone (the longest contraction) is then better cut than beside
+// the others.  30 rows of a 2048 -> 6144 block: dx and the weight gradients
+// 85 us in one launch, 45 us in two.
+template <int EPI, int MAJOR>
+cudaError_t launch_kind(const DenseProblem* p, int n, int num_sms, cudaStream_t stream, int* launches) {
+  constexpr double kHostLaunch = 2.5;  // microseconds
+  const Plan joint = plan_of<EPI, MAJOR>(p, n, num_sms);
+  ++*launches;
+  if (n > 1) {
+    const Plan first = plan_of<EPI, MAJOR>(p, 1, num_sms), others = plan_of<EPI, MAJOR>(p + 1, n - 1, num_sms);
+    if (first.us + others.us + kHostLaunch < joint.us) {
+      ++*launches;
+      cudaError_t err = launch_planned<EPI, MAJOR>(p, 1, first, num_sms, stream);
+      if (err != cudaSuccess) return err;
+      return launch_planned<EPI, MAJOR>(p + 1, n - 1, others, num_sms, stream);
+    }
+  }
+  return launch_planned<EPI, MAJOR>(p, n, joint, num_sms, stream);
 }
 
 }  // namespace dense

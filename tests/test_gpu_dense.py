@@ -245,6 +245,7 @@ FFN_BWD = [
     (333, 1016, 520, "gelu_tanh", False, HF, 16),
     (300, 72, 1032, "relu", True, BF, 0),
     (1030, 264, 136, "none", False, BF, 0),
+    (3, 2040, 4096, "relu", True, BF, 0),     # dx in a launch of its own
 ]
 
 
