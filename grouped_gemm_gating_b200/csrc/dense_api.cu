@@ -434,7 +434,9 @@ moe_status moe_ffn_backward(const uint16_t* x, int64_t ldx, int64_t T, int d, co
   return launch_gradients(jobs, n, sms, s, launches);
 }
 
-size_t moe_grad_plan_size(int n) { return n < 1 || n > (1 << 24) ? 0 : static_cast<size_t>(n) * sizeof(moe::ClipEntry); }
+size_t moe_grad_plan_size(int n) {
+  return n < 1 || n > (1 << 24) ? 0 : static_cast<size_t>(n) * sizeof(moe::ClipEntry);
+}
 
 size_t moe_grad_workspace_size(void) { return moe::kClipMaxBlocks * sizeof(double); }
 

@@ -452,7 +452,8 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
         }
       }
       // what was asked for lands, what was stored has left, before shared memory is given up
-      for (int i = stored; i < asked; ++i) ptx::mbar_wait_bounded(&my_ready[set_of(i)], phase_of(i), never, kDrainLimitNs);
+      for (int i = stored; i < asked; ++i)
+        ptx::mbar_wait_bounded(&my_ready[set_of(i)], phase_of(i), never, kDrainLimitNs);
       ptx::bulk_wait();
     }
   } else {

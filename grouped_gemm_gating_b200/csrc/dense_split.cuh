@@ -279,7 +279,8 @@ __global__ void __launch_bounds__(SplitCfg<EPI, MAJOR, BT>::kThreads)
         float4 p[kS];
 #pragma unroll
         for (int s = 0; s < kS; ++s)
-          p[s] = kS == 1 ? *reinterpret_cast<const float4*>(part + t * C::kPartStride + c) : ptx::ld_cluster_f4(base[s] + off);
+          p[s] = kS == 1 ? *reinterpret_cast<const float4*>(part + t * C::kPartStride + c)
+                         : ptx::ld_cluster_f4(base[s] + off);
         v[0] = f2(p[0].x, p[0].y);
         v[1] = f2(p[0].z, p[0].w);
 #pragma unroll
@@ -306,7 +307,8 @@ __global__ void __launch_bounds__(SplitCfg<EPI, MAJOR, BT>::kThreads)
           if constexpr (EPI == kDenseLinear) {
             if (jb.residual != nullptr)
               x0[k] = *reinterpret_cast<const uint2*>(jb.residual + rows[k] * jb.ldr + cols[k]);
-            if (MAJOR == kMajorKK && jb.bias != nullptr) x1[k] = *reinterpret_cast<const uint2*>(jb.bias + cols[k]);
+            if (MAJOR == kMajorKK && jb.bias != nullptr)
+              x1[k] = *reinterpret_cast<const uint2*>(jb.bias + cols[k]);
           } else if constexpr (EPI == kDenseGateGrad) {
             const uint16_t* p = jb.pre + rows[k] * jb.ldp + cols[k];
             x0[k] = *reinterpret_cast<const uint2*>(p);
