@@ -371,7 +371,8 @@ cudaError_t launch_clip_scale(const ClipEntry* plan, int n, int64_t chunks, int 
                               const double* partial, float* norm, int32_t* status, int num_sms, cudaStream_t stream,
                               int* launches) {
   const dim3 grid(clip_blocks(chunks, num_sms, kScaleBlocksPerSm));
-  cudaError_t err = launch_pdl(scale_kernel, grid, dim3(kThreads), 0, stream, plan, n, chunks, clip_run(chunks, num_sms), norm_type, max_norm, partial,
+  cudaError_t err = launch_pdl(scale_kernel, grid, dim3(kThreads), 0, stream, plan, n, chunks,
+                               clip_run(chunks, num_sms), norm_type, max_norm, partial,
                                clip_blocks(chunks, num_sms, kNormBlocksPerSm), norm, status);
   if (err == cudaSuccess) ++*launches;
   return err;
