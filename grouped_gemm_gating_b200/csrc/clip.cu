@@ -244,6 +244,15 @@ __global__ void __launch_bounds__(kThreads, kNormBlocksPerSm)
   if (threadIdx.x == 0) partial[blockIdx.x] = s;
 }
 
+// The norm counts as finite when the fp32 value that the caller sees is: two
+// values of 3e38 are finite, their norm is reported as infinity.
+__device__ __forceinline__ bool norm_finite(double v) { return isfinite(static_cast<float>(v)); }
+
+__device__ __forceinline__ void report_norm(double v, float* norm, int32_t* status) {
+  *norm = static_cast<float>(v);
+  if (!norm_finite(v)) set_status(status, MOE_ERR_NONFINITE);
+}
+
 __global__ void __launch_bounds__(kThreads) norm_finish_kernel(const double* partial, int n,
                                                                int norm_type, float* norm, int32_t* status) {
   __shared__ double smem[kThreads / kWarp];
@@ -252,10 +261,7 @@ __global__ void __launch_bounds__(kThreads) norm_finish_kernel(const double* par
   const bool l2 = norm_type == MOE_NORM_L2;
   double v = reduce_partials(partial, n, l2, smem);
   if (l2) v = sqrt(v);
-  if (threadIdx.x == 0) {
-    *norm = static_cast<float>(v);
-    if (!isfinite(v)) set_status(status, MOE_ERR_NONFINITE);
-  }
+  if (threadIdx.x == 0) report_norm(v, norm, status);
 }
 
 __global__ void __launch_bounds__(kThreads, kScaleBlocksPerSm)
@@ -267,13 +273,9 @@ __global__ void __launch_bounds__(kThreads, kScaleBlocksPerSm)
   const bool l2 = norm_type == MOE_NORM_L2;
   double v = reduce_partials(partial, n_partial, l2, smem);
   if (l2) v = sqrt(v);
-  const bool finite = isfinite(v);
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
-    *norm = static_cast<float>(v);
-    if (!finite) set_status(status, MOE_ERR_NONFINITE);
-  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) report_norm(v, norm, status);
   const double cd = max_norm / (v + 1e-6);
-  const float c = finite && cd < 1.0 ? static_cast<float>(cd) : 1.0f;
+  const float c = norm_finite(v) && cd < 1.0 ? static_cast<float>(cd) : 1.0f;
   int near = n - 1;
   const int64_t runs = (chunks + run - 1) / run;
   for (int64_t r = runs - 1 - blockIdx.x; r >= 0; r -= gridDim.x) {

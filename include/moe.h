@@ -566,8 +566,9 @@ MOE_API size_t moe_grad_workspace_size(void);
  * moe_grad_clip -- the same norm, then every tensor scaled by
  * c = min(1, max_norm / (norm + 1e-6)) in fp32 and rounded once into its
  * target; with c = 1 values are copied, and tensors in place are not touched.
- * max_norm > 0 (infinity: never scales).  If the norm is NaN or infinite,
- * dev_status becomes MOE_ERR_NONFINITE, norm[0] holds it and c = 1.
+ * max_norm > 0 (infinity: never scales).  If norm[0] is NaN or infinite (a
+ * norm beyond fp32's range among them), dev_status becomes MOE_ERR_NONFINITE
+ * and c = 1.
  */
 MOE_API moe_status moe_grad_norm(const void* plan, int n, int64_t chunks, moe_norm_type type, float* norm,
                          void* ws, size_t ws_bytes, int32_t* dev_status, moe_stream_t stream);

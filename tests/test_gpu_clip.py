@@ -137,6 +137,33 @@ def test_nonfinite_norm_is_flagged_and_scales_nothing(bad, kind, where):
         assert torch.equal(torch.nan_to_num(g), torch.nan_to_num(k))
 
 
+@pytest.mark.parametrize("dtype", [FP, BF])
+@pytest.mark.parametrize("value,n,finite", [(3e38, 2, False), (3e38, 1, True), (3e38, 5000, False), (2e38, 2, True)])
+def test_norm_beyond_fp32(dtype, value, n, finite):
+    """Finite gradients whose L2 norm fp32 cannot hold: reported as infinite,
+    flagged and not scaled.  The largest norms that it can hold still scale."""
+    g = torch.zeros(6000, dtype=dtype, device="cuda")
+    g[100:100 + n] = value
+    keep = g.clone()
+    v = float(g[100])
+    for call in ("norm", "clip"):
+        plan = M.GradClip([g])
+        norm = float(plan.norm() if call == "norm" else plan.clip(1e38))
+        if finite:
+            assert M.moe_read_status(plan.status) == 0
+            assert abs(norm - v * math.sqrt(n)) <= 2.0 ** -21 * norm
+        else:
+            assert norm == math.inf
+            assert M.status_name(M.moe_read_status(plan.status)) == "MOE_ERR_NONFINITE"
+        if call == "clip" and finite:
+            want = keep.double() * (1e38 / (v * math.sqrt(n)))
+            # c, its product and the output's rounding
+            assert bool(((g.double() - want).abs() <= (2.0 ** -20 + U32[dtype] * 1.0001) * want).all())
+        else:
+            assert torch.equal(g, keep)
+    assert float(M.GradClip([keep]).norm(M.NORM_MAX)) == v
+
+
 def test_same_on_every_call_and_in_a_graph():
     grads = tensors([200_001, 3000, 5], (BF, FP), 6)
     outs = [torch.empty_like(g) for g in grads]
