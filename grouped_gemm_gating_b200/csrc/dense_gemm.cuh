@@ -371,8 +371,6 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
       // arrives on both CTAs' mma_done
       ptx::mma_commit_pair(mma_done);
       if (!ptx::mbar_wait_bounded(mma_done, 0u, never, kDrainLimitNs)) fail();
-    } else if (rank != 0 && lane == 0) {
-      if (!ptx::mbar_wait_cluster_bounded(mma_done, 0u, never, kDrainLimitNs)) fail();
     }
   } else if (warp >= 10) {
     // ------------------------------------------------ mover of one epilogue group's data
@@ -623,6 +621,11 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
   __syncthreads();
   ptx::cluster_sync();  // the peer's last arrivals and reads are done
   if (warp == 1) {
+    // The odd CTA outlives the last commit's arrival on its own barrier.  The
+    // even CTA has seen its half by now: the wait's limit does not run while
+    // the tiles are worked on, however long they take together.
+    if (rank != 0 && !ptx::mbar_wait_cluster_bounded(mma_done, 0u, never, kDrainLimitNs)) fail();
+    __syncwarp();
     ptx::tc_fence_after();
     ptx::tmem_dealloc_pair(tmem_base, C::kTmemCols);
   }

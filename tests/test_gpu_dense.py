@@ -382,6 +382,34 @@ def test_offsets_past_32_bits():
     assert torch.equal(out[:5], (x[:5].float() @ w.float().T).to(BF))
 
 
+def test_product_of_more_than_a_second():
+    """1.9e15 operations in one launch, at least 1.2 s at the rate that a step
+    of k takes: the kernel's waits run per tile, not per launch.  Values +-1:
+    sums are whole numbers below 2^24, exact in fp32, then rounded once."""
+    n = 98_816
+    gen = torch.Generator(device="cuda").manual_seed(47)
+
+    def signs():
+        t = torch.empty(n, n, dtype=BF, device="cuda")
+        for i in range(0, n, 8192):
+            part = t[i:i + 8192]
+            part.copy_(torch.randint(0, 2, part.shape, generator=gen, device="cuda", dtype=torch.int8) * 2 - 1)
+        return t
+
+    x, w = signs(), signs()
+    out = torch.empty(n, n, dtype=BF, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    M.moe_linear(x, w, out, dev_status=status)
+    ok(status)
+    rows = torch.cat([torch.arange(0, n, 3001, device="cuda"), torch.arange(n - 3, n, device="cuda")])
+    xs = x[rows].float()
+    for i in range(0, n, 8192):
+        want = (xs @ w[i:i + 8192].float().T).to(BF)
+        assert torch.equal(out[rows, i:i + 8192], want)
+    del x, w, out
+    torch.cuda.empty_cache()
+
+
 @pytest.mark.parametrize("T,N", [(4, 512), (300, 512), (9000, 2048)])
 def test_timeout_is_reported(T, N):
     """A wait that runs out sets the status; the next call works.  Few rows,
