@@ -590,7 +590,7 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
                   F2 slope;
                   const F2 v = act_value_slope<decltype(act)::value>(g[j], &slope);
                   h[j] = v * up[j];
-                  dg[j] = dh * up[j] * slope;
+                  dg[j] = dh * (up[j] * slope);  // dh u alone may overflow where the slope is 0
                   du[j] = dh * v;
                 }
                 *cell(b, s * 4 + i) = pack8<kFp16>(dg);

@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(SplitCfg<EPI, MAJOR, BT>::kThreads)
                 F2 slope;
                 const F2 a = act_value_slope<kAct>(g[j], &slope);
                 h[j] = a * u[j];
-                dg[j] = v[k][j] * u[j] * slope;
+                dg[j] = v[k][j] * (u[j] * slope);  // dh u alone may overflow where the slope is 0
                 du[j] = v[k][j] * a;
               }
               store4<kFp16>(jb.out + row * jb.ldo + col, dg);

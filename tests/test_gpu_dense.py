@@ -284,6 +284,27 @@ def test_ffn_backward(T, d_, F, name, res, dtype, pad):
         assert np.linalg.norm(np64(got) - ref) <= 2 * U[dtype] * norm + 1e-6
 
 
+@pytest.mark.parametrize("name,g", [("relu", -1.0), ("relu2", -1.0), ("silu", -200.0), ("gelu", -40.0),
+                                    ("gelu_tanh", -40.0)])
+@pytest.mark.parametrize("T", [4, 9000])  # the split kernel and the pair kernel
+def test_ffn_backward_of_a_closed_gate(T, name, g):
+    """Where the gate's value and slope are 0, large finite dh and u (their
+    product beyond fp32) give zero gradients, not 0 * infinity."""
+    dd, F = 512, 1024
+    e = lambda *s: torch.zeros(s, dtype=BF, device="cuda")  # noqa: E731
+    x, dout, pre = e(T, dd), e(T, dd), e(T, 2 * F)
+    w13, w2 = e(2 * F, dd) + 1, e(dd, F)
+    x += 1
+    dout[:, 0], w2[0] = 1e20, 1.0      # dh = 1e20
+    pre[:, :F], pre[:, F:] = g, 1e20
+    dx, dw13, dw2 = e(T, dd) + 7, e(2 * F, dd) + 7, e(dd, F) + 7
+    ws = torch.empty(M.moe_ffn_backward_workspace_size(T, dd, F), dtype=torch.uint8, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    M.moe_ffn_backward(x, w13, w2, pre, dout, ws, dx, dw13, dw2, EPI[name], dev_status=status)
+    ok(status)
+    assert not any(bool(t.any()) for t in (dx, dw13, dw2))
+
+
 def test_ffn_gradients_against_differences():
     """The whole step's gradients against central differences of the oracle's
     forward in fp64, on the same values: directions drawn at random."""
