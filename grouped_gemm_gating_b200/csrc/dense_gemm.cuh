@@ -478,6 +478,7 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
         fail();
         break;
       }
+      __syncwarp();  // orders what lane 0 waited for before the other lanes' reads (a vote orders nothing)
       ptx::tc_fence_after();
       const uint32_t t_acc =
           tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(abuf * BN + p.acc);
@@ -497,6 +498,7 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
           ok = false;
           break;
         }
+        __syncwarp();  // the same for the residual, or g and u, that TMA wrote
 #pragma unroll 1
         for (int s = 0; s < 2; ++s) {
           const int col = p.col + c * 64 + s * 32;

@@ -386,6 +386,31 @@ def test_same_on_every_call_and_stream():
             assert torch.equal(a, c)
 
 
+def test_pair_kernel_repeats():
+    """Large batches: what TMA brings for the epilogue (a residual, the kept
+    g and u) is seen by every lane of a warp, call after call."""
+    d = Draw(32, BF)
+    T, K, N = 9001, 264, 2056
+    x, w, r = d.whole((T, K)), d.whole((N, K), K ** -0.5), d.whole((T, N))
+    b = M.FFNBuffers(T, K, 1032, train=True)
+    w13, w2, dout = d.whole((2064, K), 0.05), d.whole((K, 1032), 0.05), d.whole((T, K))
+    out = torch.empty_like(r)
+    names = ("out", "pre", "dx", "dw13", "dw2")
+    want = None
+    for _ in range(20):
+        M.moe_linear(x, w, out, None, r)
+        b.forward(x, w13, w2, x)
+        b.backward(x, w13, w2, dout, dx_residual=dout)
+        got = [out.clone()] + [getattr(b, n).clone() for n in names]
+        want = want or got
+        for a, c in zip(got, want):
+            assert torch.equal(a, c)
+    ok(b.status)
+    X, W = np64(x[-300:]), np64(w)
+    ref, zref = D.linear(X, W, None, np64(r[-300:]))
+    check(want[0][-300:], ref, linear_bounds(X, W, zref, "none")[0] + 2.0 ** -23 * np.abs(ref), "last rows", BF)
+
+
 def test_offsets_past_32_bits():
     """An output of more than 2^31 elements, its last rows checked."""
     T, K, N = (1 << 18) + 100, 8, 8200
