@@ -303,8 +303,10 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   return v;
 }
 
-// Cluster-wide barrier of all threads of all CTAs.
+// Cluster-wide barrier of all threads of all CTAs.  The aligned forms want
+// whole warps: lanes that left a loop or a branch at different times join first.
 __device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 

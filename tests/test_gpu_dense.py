@@ -386,6 +386,30 @@ def test_same_on_every_call_and_stream():
             assert torch.equal(a, c)
 
 
+@pytest.mark.parametrize("T", [1, 3, 5, 13])
+def test_split_kernel_repeats(T):
+    """Rows and shares of columns that leave the lanes of a warp a different
+    number of items each, before the cluster's barrier; odd column sums."""
+    d = Draw(33, BF)
+    K, N = 1000, 1848
+    x, w, r, dout = d.whole((T, K)), d.whole((N, K), K ** -0.5), d.whole((T, N)), d.whole((T, N))
+    out, dx = torch.empty_like(r), torch.empty_like(x)
+    dw, db = torch.empty_like(w), torch.empty(N, dtype=BF, device="cuda")
+    want = None
+    for _ in range(50):
+        M.moe_linear(x, w, out, None, r)
+        M.moe_linear_backward(x, w, dout, dx, dw, db)
+        got = [t.clone() for t in (out, dx, dw, db)]
+        want = want or got
+        for a, c in zip(got, want):
+            assert torch.equal(a, c)
+    X, W = np64(x), np64(w)
+    ref, zref = D.linear(X, W, None, np64(r))
+    check(want[0], ref, linear_bounds(X, W, zref, "none")[0] + 2.0 ** -23 * np.abs(ref), "out", BF)
+    G = np64(dout)
+    check(want[3], G.sum(0), T * ADD * np.abs(G).sum(0), "dbias", BF)
+
+
 def test_pair_kernel_repeats():
     """Large batches: what TMA brings for the epilogue (a residual, the kept
     g and u) is seen by every lane of a warp, call after call."""
