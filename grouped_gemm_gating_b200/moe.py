@@ -529,6 +529,8 @@ class LinearBuffers:
     and the backward's workspace."""
 
     def __init__(self, T, K, N, act=EPI_NONE, dtype=torch.bfloat16, train=False, bias=False, device="cuda"):
+        if moe_linear_backward_workspace_size(T, K, N, EPI_SILU if act == EPI_NONE else act) == 0:
+            raise ValueError("unsupported layer shape or activation")
         self.T, self.K, self.N, self.act = T, K, N, act
         dev = torch.device(device)
         kw = dict(dtype=dtype, device=dev)
@@ -597,6 +599,8 @@ class FFNBuffers:
     the gradients and the backward's workspace."""
 
     def __init__(self, T, d, F, act=EPI_SILU, dtype=torch.bfloat16, train=False, device="cuda"):
+        if moe_ffn_backward_workspace_size(T, d, F) == 0 or not EPI_NONE <= act <= EPI_RELU2:
+            raise ValueError("unsupported block shape or activation")
         self.T, self.d, self.F, self.act = T, d, F, act
         dev = torch.device(device)
         kw = dict(dtype=dtype, device=dev)
@@ -609,10 +613,7 @@ class FFNBuffers:
             self.dx = torch.empty((T, d), **kw)
             self.dw13 = torch.empty((2 * F, d), **kw)
             self.dw2 = torch.empty((d, F), **kw)
-            n = moe_ffn_backward_workspace_size(T, d, F)
-            if n == 0:
-                raise ValueError("unsupported block shape")
-            self.ws = torch.empty(n, dtype=torch.uint8, device=dev)
+            self.ws = torch.empty(moe_ffn_backward_workspace_size(T, d, F), dtype=torch.uint8, device=dev)
 
     def forward(self, x, w13, w2, residual=None):
         moe_ffn(x, w13, w2, self.h, self.out, self.act, residual, self.pre, self.status)

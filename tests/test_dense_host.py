@@ -215,3 +215,19 @@ def test_binding_refuses_cpu_tensors():
         M.GradClip([x])
     with pytest.raises(ValueError):
         M.GradClip([])
+
+
+@pytest.mark.parametrize("train", [False, True])
+def test_buffers_refuse_what_no_call_takes(lib, train):
+    """A shape or activation that every call would refuse is refused when the
+    buffers are made, before anything is allocated for it."""
+    for T, K, N, act in ((4, 60, 32, 0), (4, 64, 36, 1), (-1, 64, 32, 0), (4, 1 << 18, 32, 0), ((1 << 24) + 1, 8, 8, 2),
+                         (4, 64, 32, 6), (4, 64, 32, -1)):
+        with pytest.raises(ValueError):
+            M.LinearBuffers(T, K, N, act, train=train, device="cpu")
+        with pytest.raises(ValueError):
+            M.FFNBuffers(T, K, N, act, train=train, device="cpu")
+    for T in (0, 4):  # shapes that calls take
+        b = M.LinearBuffers(T, 64, 32, train=train, device="cpu")
+        assert b.out.shape == (T, 32) and b.ws is None
+        assert M.FFNBuffers(T, 64, 32, train=train, device="cpu").h.shape == (T, 32)
