@@ -284,6 +284,32 @@ def test_ffn_backward(T, d_, F, name, res, dtype, pad):
         assert np.linalg.norm(np64(got) - ref) <= 2 * U[dtype] * norm + 1e-6
 
 
+# The same tests at sizes of which every launch runs on CTA pairs (asserted
+# without a GPU in test_dense_plan.py): odd token counts, widths that end inside
+# a tile and inside 64 columns, a last round of whole tiles and of halves, rounds
+# that reuse the epilogue's buffers, both types.
+LINEAR_BWD_PAIRS = [
+    (4700, 1032, 2056, "gelu", True, True, HF, 8),
+    (3001, 1032, 2312, "relu2", True, False, BF, 0),
+]
+FFN_BWD_PAIRS = [
+    (4097, 520, 1256, "silu", True, BF, 8),
+    (4097, 264, 2312, "gelu", True, HF, 0),
+    (3001, 520, 2312, "gelu_tanh", False, HF, 16),
+    (2100, 1032, 1032, "relu2", True, BF, 0),
+]
+
+
+@pytest.mark.parametrize("case", LINEAR_BWD_PAIRS, ids=str)
+def test_linear_backward_on_pairs(case):
+    test_linear_backward(*case)
+
+
+@pytest.mark.parametrize("case", FFN_BWD_PAIRS, ids=str)
+def test_ffn_backward_on_pairs(case):
+    test_ffn_backward(*case)
+
+
 @pytest.mark.parametrize("name,g", [("relu", -1.0), ("relu2", -1.0), ("silu", -200.0), ("gelu", -40.0),
                                     ("gelu_tanh", -40.0)])
 @pytest.mark.parametrize("T", [4, 9000])  # the split kernel and the pair kernel
