@@ -8,6 +8,7 @@ import subprocess
 import pytest
 
 from grouped_gemm_gating_b200 import build as B
+from test_gpu_activations import BACKWARD, FORWARD
 from test_gpu_dense import FFN, FFN_BWD, FFN_BWD_PAIRS, LINEAR, LINEAR_BWD, LINEAR_BWD_PAIRS
 
 PROGRAM = r"""
@@ -106,3 +107,9 @@ def test_small_gradients_run_on_the_split_kernel(plan):
         for c in cases:
             if c[0] <= 300 and max(c[1:3]) <= 1100:
                 assert set(plan(op, c)) == {"split"}, c
+
+
+def test_activation_cases_reach_both_kernels(plan):
+    for op, (small, large) in (("linear", FORWARD), ("ffn", FORWARD), ("ffn_backward", BACKWARD)):
+        no_residual = ("silu", False, False)
+        assert plan(op, small + no_residual)[0] == "split" and plan(op, large + no_residual)[0] == "pair", op
