@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
           }
         }
         if (!ok) break;
-        ptx::mma_commit_pair(&tfull[abuf]);  // with nothing to contract: arrives at once
+        ptx::mma_commit_pair(&tfull[abuf]);
         if (++abuf == 2) {
           abuf = 0;
           aphase ^= 1u;
@@ -511,14 +511,9 @@ __global__ void __launch_bounds__(Cfg<EPI, MAJOR>::kNumThreads, 1)
               for (int i = 0; i < 4; ++i)
                 if (col + 8 * i < jb.N) bias[i] = *reinterpret_cast<const uint4*>(jb.bias + col + 8 * i);
             }
-            if (jb.nk > 0) {
-              tmem_ld(at, a);
-              ptx::tmem_wait_ld();
-              pin(a);
-            } else {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) a[j] = 0u;
-            }
+            tmem_ld(at, a);
+            ptx::tmem_wait_ld();
+            pin(a);
             with_act(MAJOR == kMajorKK && last_pass ? args.act : MOE_EPI_NONE, [&](auto act) {
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
@@ -675,8 +670,7 @@ template <int EPI, int MAJOR, bool kFp16>
 bool make_job(const DenseProblem& p, Job* a) {
   using C = Cfg<EPI, MAJOR>;
   const bool a_mn = p.major == kMajorMN, b_mn = p.major != kMajorKK;
-  const uint64_t M = p.M, N = p.N;
-  const uint64_t K = p.K > 0 ? p.K : 8;  // with nothing to contract no load is issued
+  const uint64_t M = p.M, N = p.N, K = p.K;
   bool ok = a_mn ? encode_rows(&a->tm_a, kFp16, p.a, K, M, p.lda, 64, 64)
                  : encode_rows(&a->tm_a, kFp16, p.a, M, K, p.lda, 64, 128);
   if (EPI == kDenseGate) {

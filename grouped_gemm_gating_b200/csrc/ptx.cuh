@@ -162,25 +162,6 @@ __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.comm
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-// Barrier `id` among `threads` threads (whole warps).
-__device__ __forceinline__ void named_sync(int id, int threads) {
-  asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-
-// The same, returning whether any thread passed true.
-__device__ __forceinline__ bool named_sync_or(int id, int threads, bool v) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %3, 0;\n\t"
-      "barrier.cta.red.or.pred q, %1, %2, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(id), "r"(threads), "r"(v ? 1u : 0u)
-      : "memory");
-  return r != 0;
-}
-
 // L2 policy that makes the lines a load brings in the first to be evicted.
 __device__ __forceinline__ uint64_t l2_policy_evict_first() {
   uint64_t p;
