@@ -78,8 +78,8 @@ def plan(tmp_path_factory):
 
     def ask(op, case):
         (T, K, N), residual = case[:3], case[4 if op.startswith("ffn") else 5]
-        r = subprocess.run([exe], input=f"{op} {T} {K} {N} {int(residual)}\n", capture_output=True, text=True, check=True)
-        return r.stdout.split()
+        line = f"{op} {T} {K} {N} {int(residual)}\n"
+        return subprocess.run([exe], input=line, capture_output=True, text=True, check=True).stdout.split()
 
     return ask
 
