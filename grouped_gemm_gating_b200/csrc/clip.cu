@@ -19,6 +19,9 @@
 // neither large nor tiny gradients overflow or vanish.  Every block's sum is
 // one partial; both kernels add the partials in a fixed order: the norm is
 // the same on every call.
+//
+// Targets that lie differently within 16 bytes than their sources are written
+// one value at a time: 200 M bf16 values 785 us, aligned alike 207 us.
 #include "common.cuh"
 #include "dense.h"
 #include "epilogue.cuh"

@@ -177,7 +177,11 @@ moe_status moe_linear(const uint16_t* x, int64_t ldx, int64_t T, int K, const ui
   if (bias && (st = check_mat(mb)) != MOE_OK) return st;
   if (residual && (st = check_mat(mr)) != MOE_OK) return st;
   if (pre && (st = check_mat(mp)) != MOE_OK) return st;
-  // out may be the residual itself: a thread reads an element before it writes it
+  // out may be the residual itself.  The pair kernel fetches the residual of a
+  // chunk (a box of 128 rows x 64 columns) some chunks ahead and stores the
+  // chunk's result later: a box is read before it is written, and no two chunks
+  // share an element.  In the split kernel a thread reads an element before it
+  // writes it.
   if (!disjoint({mo, mp}, {mx, mw, mb}) || share(mp, mr) || (share(mo, mr) && !same(mo, mr)))
     return MOE_ERR_INVALID_ARG;
   const int sms = num_sms_current_device();

@@ -58,7 +58,9 @@ constexpr uint64_t kDrainGraceNs = 50000;
 // side of the grid of tiles is kept whole, so that its operand stays in L2
 // and the other one passes once (measured with groups of 2, 8 and 16: 64 x 8
 // tiles at K = 8192 352, 359 and 368 us, a gate of 16 x 96 at K = 4096 585,
-// 514 and 502 us, 32 x 32 at K = 8192 763, 693 and 720 us).
+// 514 and 502 us, 32 x 32 at K = 8192 763, 693 and 720 us).  Three grids at
+// long contractions: the rule goes by tiles alone, not by the bytes that K
+// makes of them, and short contractions were not measured.
 inline int group_rows(int n_mt, int n_nt) { return n_nt <= 8 ? 2 : n_mt <= 16 ? 16 : 8; }
 
 struct Job {

@@ -578,9 +578,11 @@ cudaError_t launch_planned(const DenseProblem* p, int n, const Plan& plan, int n
 }
 
 // One launch, or two where that saves more than a launch costs the host: the
-// first job alone (the longest contraction) is then better cut than beside
-// the others.  30 rows of a 2048 -> 6144 block: dx and the weight gradients
-// 85 us in one launch, 45 us in two.
+// first job alone is then better cut than beside the others.  It is the one
+// of the longest contraction: dx for few tokens (its contraction is the layer's
+// width, twice that of a gated block), a weight gradient where the tokens are
+// more.  30 rows of a 2048 -> 6144 block: dx and the weight gradients 85 us in
+// one launch, 45 us in two.
 template <int EPI, int MAJOR>
 cudaError_t launch_kind(const DenseProblem* p, int n, int num_sms, cudaStream_t stream, int* launches) {
   constexpr double kHostLaunch = 2.5;  // microseconds

@@ -526,7 +526,8 @@ def moe_linear_backward(x, w, dout, dx=None, dw=None, dbias=None, act=EPI_NONE, 
 class LinearBuffers:
     """Device buffers of one linear layer's shape, allocated once (plumbing
     only): the output and, for training, the pre-activation, the gradients
-    and the backward's workspace."""
+    and the backward's workspace.  T is fixed: for batches of several sizes
+    allocate for the largest and pass the first rows to moe_linear."""
 
     def __init__(self, T, K, N, act=EPI_NONE, dtype=torch.bfloat16, train=False, bias=False, device="cuda"):
         if moe_linear_backward_workspace_size(T, K, N, EPI_SILU if act == EPI_NONE else act) == 0:
@@ -596,7 +597,8 @@ def moe_ffn_backward(x, w13, w2, pre, dout, ws, dx=None, dw13=None, dw2=None, ac
 class FFNBuffers:
     """Device buffers of one dense gated block's shape, allocated once
     (plumbing only): h, the output and, for training, the kept projections,
-    the gradients and the backward's workspace."""
+    the gradients and the backward's workspace.  T is fixed: for batches of
+    several sizes allocate for the largest and pass the first rows to moe_ffn."""
 
     def __init__(self, T, d, F, act=EPI_SILU, dtype=torch.bfloat16, train=False, device="cuda"):
         if moe_ffn_backward_workspace_size(T, d, F) == 0 or not EPI_NONE <= act <= EPI_RELU2:
@@ -630,7 +632,10 @@ class GradClip:
     """Global norm and clipping of a set of gradient tensors: the plan (which
     holds the tensors' addresses, and the tensors with them), its workspace
     and the norm.  outs: where the scaled tensors go (default: in place).
-    Make a new one when a gradient buffer is replaced."""
+    Make a new one when a gradient buffer is replaced.  The plan is written on
+    the stream that is current then; a call on another stream waits for it as
+    for any tensor, and two calls of one GradClip do not run at once (they
+    share its workspace)."""
 
     def __init__(self, grads, outs=None):
         grads = list(grads)
